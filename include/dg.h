@@ -248,6 +248,159 @@ int dg_bind_stream_workspace(void* stream, void* workspace, size_t bytes);
  * for debugging only, and it is skipped while the stream is being captured. */
 int dg_check_grouped_layout(const int32_t* grouped_layout, int M, int num_groups);
 
+/* ---- The operators around the products --------------------------------------
+ *
+ * A router chooses each token's experts, the layout calls give every choice a
+ * row of the M-grouped (or K-grouped) products, the scatter calls move and
+ * quantise the tokens' rows there, the gather call sums the experts' results
+ * back per token, and the adapter call adds low-rank terms to (or ahead of) a
+ * dense projection.  They follow the rules above: device pointers owned by the
+ * caller, checks on the host, no synchronisation, capturable in a HIP graph
+ * after dg_init(), and the device's (or the stream's bound) workspace as
+ * scratch where a call says so.  An array of no elements may be NULL.
+ *
+ * Sums, softmax statistics and scales are fp32; bf16 results are rounded once
+ * (to nearest, ties to even).  No result depends on the order of atomics. */
+
+typedef enum { DG_F32 = 0, DG_BF16 = 1 } dg_dtype;
+typedef enum { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_score;
+
+/* Routing: for every token the top_k of num_experts by
+ *   key[e] = s[e] + bias[e],   s = softmax(logits) over the experts or sigmoid(logits),
+ * and their weights scale * s[e], divided by the sum of the chosen s if
+ * renormalize is nonzero (bias steers the choice only).  With num_groups > 1 the
+ * experts are num_groups equal runs; a group's score is the sum of its
+ * group_top (1 or 2) highest keys, and only the topk_groups highest groups'
+ * experts can be chosen.  Equal keys, and equal group scores, go to the lowest
+ * index; chosen experts come in falling order of key.
+ *   logits  logits_type [T][E]   DG_F32 or DG_BF16
+ *   bias    float [E] or NULL
+ *   topk_ids int32 [T][top_k], topk_weights float [T][top_k]   outputs
+ * An expert whose logit or key is -inf or NaN is masked: it is never chosen (a
+ * masked logit adds nothing to the softmax either, and masked experts add
+ * nothing to a group's score).  A token with fewer than top_k experts left gets
+ * id -1 and weight 0 in its last slots.  A logit of +inf counts as the largest
+ * finite value.  Chosen scores that sum to zero give weights of zero under
+ * renormalize.  E at most 1024, top_k at most 64, num_groups at most 64
+ * (DG_ERR_UNSUPPORTED otherwise); top_k <= topk_groups * E / num_groups.
+ * Returns a dg_status. */
+int dg_route_topk(const void* logits, int logits_type, const float* bias, int32_t* topk_ids, float* topk_weights,
+                  int T, int E, int top_k, int score, int num_groups, int topk_groups, int group_top,
+                  int renormalize, float scale, void* stream);
+
+/* Gradient of the routing weights with respect to the logits, for the choice
+ * made in the forward pass (ids are constants; a token's ids are distinct, and
+ * one outside [0, E) takes no part):
+ *   grad_logits[t][i] = sum_j grad_weights[t][j] * d topk_weights[t][j] / d logits[t][i]
+ *   logits, grad_logits  logits_type [T][E]; topk_ids int32 [T][top_k];
+ *   grad_weights float [T][top_k]
+ * A masked expert's gradient is 0.  Returns a dg_status. */
+int dg_route_topk_backward(const void* logits, int logits_type, const int32_t* topk_ids, const float* grad_weights,
+                           void* grad_logits, int T, int E, int top_k, int score, int renormalize, float scale,
+                           void* stream);
+
+/* The most rows that the contiguous layout of `choices` = T * top_k choices can
+ * need over num_groups experts: every expert's rows rounded up to 128.  Host
+ * only.  Returns -1 for a negative argument or a result beyond 2^31 - 1. */
+int dg_m_grouped_rows_bound(long long choices, int num_groups);
+
+/* Rows for the contiguous products.  The choices topk_ids [T][top_k] whose
+ * expert lies in [first_expert, first_expert + num_groups) are this GPU's; choice
+ * i = t * top_k + j of local expert g gets the next row of g's segment, in the
+ * order of i, and the segments follow one another by g, each starting at a
+ * multiple of 128.
+ *   grouped_layout int32 [M]   local expert of each row, -1 for rows without one
+ *   row_of   int32 [T][top_k]  each choice's row, -1 without one
+ *   slot_of  int32 [M]         each row's choice i, -1 without one
+ *   counts   int32 [num_groups]  choices per local expert, or NULL
+ * M (a multiple of 128) is the room there is: dg_m_grouped_rows_bound() rows
+ * always suffice; choices whose row would lie beyond M have none (row_of -1),
+ * and counts still counts them.  num_groups at most 1024.  Scratch: workspace
+ * (a small one costs speed only).  Returns a dg_status. */
+int dg_m_grouped_layout_contiguous(const int32_t* topk_ids, int T, int top_k, int first_expert, int num_groups, int M,
+                                   int32_t* grouped_layout, int32_t* row_of, int32_t* slot_of, int32_t* counts,
+                                   void* stream);
+
+/* Rows for the masked products: choice i of local expert g gets row
+ * g * max_m + r with r counting g's choices in the order of i; choices beyond
+ * max_m have none.
+ *   masked_m int32 [num_groups]  min(choices, max_m) per local expert
+ *   row_of   int32 [T][top_k], slot_of int32 [num_groups][max_m]   as above
+ * Returns a dg_status. */
+int dg_m_grouped_layout_masked(const int32_t* topk_ids, int T, int top_k, int first_expert, int num_groups, int max_m,
+                               int32_t* masked_m, int32_t* row_of, int32_t* slot_of, void* stream);
+
+/* Moves the tokens' rows to the experts' rows, quantised to e4m3 with one scale
+ * per row per 128 values: for every choice i = t * top_k + j with row r = row_of[i],
+ *   v = weights[i] * x[t] (x[t] without weights),  sf = max(amax, 2^-100) / 448
+ *   with amax = max |v| over the block (sf = 1 if amax = 0; with pow2_scales
+ *   rounded up to a power of two),  a[r] = e4m3_rne(clamp(v * (1/sf), -448, 448)).
+ *   x        bf16  [T][K] (16-byte aligned)
+ *   weights  float [T][top_k] or NULL
+ *   row_of, slot_of   the maps of the layout call; entries outside the range of
+ *            rows or choices are skipped
+ *   contiguous: a uint8 [M][K], sfa float [K/128][M], slot_of [M]
+ *   masked:     a uint8 [G][max_m][K], sfa float [G][K/128][max_m], slot_of [G][max_m]
+ * Rows without a choice are left as they are.  A NaN in v gives a NaN code and
+ * does not count for amax; an infinity gives its block an infinite scale and a
+ * NaN code in its own place.  K must be a multiple of 128.  Scratch: workspace.
+ * Returns a dg_status. */
+int dg_m_grouped_scatter_fp8_contiguous(const void* x, const float* weights, const int32_t* row_of,
+                                        const int32_t* slot_of, void* a, float* sfa, int T, int top_k, int M, int K,
+                                        int pow2_scales, void* stream);
+int dg_m_grouped_scatter_fp8_masked(const void* x, const float* weights, const int32_t* row_of,
+                                    const int32_t* slot_of, void* a, float* sfa, int T, int top_k, int num_groups,
+                                    int max_m, int K, int pow2_scales, void* stream);
+
+/* The same rows as an operand of the K-grouped product: one scale per column per
+ * 128 rows, and rows without a choice are zeros (128 such rows have scale 1).
+ *   x bf16 [T][N] (16-byte aligned), weights float [T][top_k] or NULL,
+ *   slot_of int32 [K], a uint8 [K][N] (16-byte aligned), sfa float [K/128][N]
+ * K (the rows, a multiple of 128) may be less than the layout's M: the segments
+ * used.  N must be a multiple of 16 (DG_ERR_UNSUPPORTED otherwise).  Returns a
+ * dg_status. */
+int dg_k_grouped_scatter_fp8(const void* x, const float* weights, const int32_t* slot_of, void* a, float* sfa, int T,
+                             int top_k, int K, int N, int pow2_scales, void* stream);
+
+/* The experts' rows back to the tokens:
+ *   d[t] = bf16_rne( c[t] + sum_j weights[t][j] * rows[row_of[t][j]] )
+ * summed in fp32 from j = 0 on, weights NULL meaning 1; a row_of outside [0, M)
+ * adds nothing, whatever its weight.  Without weights it is also the gradient
+ * of the scatter, and the scatter with weights is the gradient of this with
+ * respect to rows.
+ *   rows bf16 [M][N] (the masked form's [G][max_m][N] with M = G * max_m),
+ *   row_of int32 [T][top_k], weights float [T][top_k] or NULL,
+ *   c bf16 [T][N] or NULL (may equal d), d bf16 [T][N]
+ * Any N; top_k at most 64 (DG_ERR_UNSUPPORTED otherwise).  Returns a dg_status. */
+int dg_m_grouped_gather(const void* rows, const int32_t* row_of, const float* weights, const void* c, void* d, int T,
+                        int top_k, int M, int N, void* stream);
+
+/* Gradient of the gather with respect to its weights:
+ *   grad_weights[t][j] = sum_n grad_d[t][n] * rows[row_of[t][j]][n]   (0 without a row)
+ *   rows bf16 [M][N], grad_d bf16 [T][N], grad_weights float [T][top_k]
+ * Returns a dg_status. */
+int dg_m_grouped_gather_weight_grad(const void* rows, const int32_t* row_of, const void* grad_d, float* grad_weights,
+                                    int T, int top_k, int M, int N, void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   d[t] = bf16_rne( c[t] + scales[i] * B[i] . (A[i] . x[t]) ),   i = adapter_ids[t]
+ * A token whose id lies outside [0, num_adapters) has no adapter: d[t] = c[t].
+ * With c the projection's result it completes it; with c NULL its d is the C of
+ * the dense call.
+ *   x  bf16 [T] rows of K values, ldx apart (16-byte aligned, ldx % 8 == 0)
+ *   a  bf16 [num_adapters][R][K], b bf16 [num_adapters][N][R] (16-byte aligned)
+ *   scales float [num_adapters] or NULL (1), adapter_ids int32 [T]
+ *   c  bf16 [T] rows of N values, ldc apart, or NULL (0); may equal d
+ *   d  bf16 [T] rows of N values, ldd apart
+ * A . x is summed in fp32 and kept to 16 bits of mantissa or more.  K must be a
+ * multiple of 128, R a multiple of 8 and at most 256 (adapters of lower rank are
+ * filled up with zeros); any N.  num_adapters at most 1024 (DG_ERR_UNSUPPORTED
+ * otherwise).  Scratch: workspace (DG_ERR_UNSUPPORTED if a bound one has no room
+ * for 16 tokens).  Returns a dg_status. */
+int dg_lora_bf16_nt(const void* x, int ldx, const void* a, const void* b, const float* scales,
+                    const int32_t* adapter_ids, const void* c, int ldc, void* d, int ldd, int T, int N, int K, int R,
+                    int num_adapters, void* stream);
+
 /* Prepares per-device state for the current HIP device (device properties and
  * the split-K workspace, allocated once and kept until the process ends).
  * Calls above do this lazily on first use; call dg_init() first when the

@@ -1,6 +1,8 @@
 """FP8 (e4m3) block-scaled GEMM (NT, and NN/TN/TT with K-major operands), with
 M-grouped MoE forms, the K-grouped TN form and an FP8 x FP4 GEMM, for AMD
-MI355X (gfx950).  The kernels live in libdg.so behind the C ABI of
+MI355X (gfx950), with the operators around them: the router, the experts' row
+layouts, the quantising scatter and the weighted gather, and low-rank adapters
+beside a dense projection.  The kernels live in libdg.so behind the C ABI of
 include/dg.h; this package is its Python binding."""
 from ._lib import (  # noqa: F401
     DGError,
@@ -17,10 +19,21 @@ from ._lib import (  # noqa: F401
     dg_fp8_gemm_tt,
     dg_init,
     dg_k_grouped_fp8_gemm_tn_contiguous,
+    dg_k_grouped_scatter_fp8,
+    dg_lora_bf16_nt,
     dg_m_grouped_fp8_fp4_gemm_nt_contiguous,
     dg_m_grouped_fp8_fp4_gemm_nt_masked,
     dg_m_grouped_fp8_gemm_nt_contiguous,
     dg_m_grouped_fp8_gemm_nt_masked,
+    dg_m_grouped_gather,
+    dg_m_grouped_gather_weight_grad,
+    dg_m_grouped_layout_contiguous,
+    dg_m_grouped_layout_masked,
+    dg_m_grouped_rows_bound,
+    dg_m_grouped_scatter_fp8_contiguous,
+    dg_m_grouped_scatter_fp8_masked,
+    dg_route_topk,
+    dg_route_topk_backward,
     dg_version,
     load,
 )

@@ -31,6 +31,17 @@ EXPORTED = [
     "dg_m_grouped_fp8_fp4_gemm_nt_contiguous",
     "dg_m_grouped_fp8_fp4_gemm_nt_masked",
     "dg_k_grouped_fp8_gemm_tn_contiguous",
+    "dg_route_topk",
+    "dg_route_topk_backward",
+    "dg_m_grouped_rows_bound",
+    "dg_m_grouped_layout_contiguous",
+    "dg_m_grouped_layout_masked",
+    "dg_m_grouped_scatter_fp8_contiguous",
+    "dg_m_grouped_scatter_fp8_masked",
+    "dg_k_grouped_scatter_fp8",
+    "dg_m_grouped_gather",
+    "dg_m_grouped_gather_weight_grad",
+    "dg_lora_bf16_nt",
     "dg_choose_config",
     "dg_check_grouped_layout",
     "dg_bind_stream_workspace",
@@ -74,6 +85,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.dg_m_grouped_fp8_fp4_gemm_nt_masked.restype = ci
         lib.dg_k_grouped_fp8_gemm_tn_contiguous.argtypes = [vp, fp, vp, fp, vp, vp, ci, ci, ci, vp, vp]
         lib.dg_k_grouped_fp8_gemm_tn_contiguous.restype = ci
+        cf = ctypes.c_float
+        for name, types in {
+            "dg_route_topk": [vp, ci, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, ci, cf, vp],
+            "dg_route_topk_backward": [vp, ci, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp],
+            "dg_m_grouped_rows_bound": [ctypes.c_longlong, ci],
+            "dg_m_grouped_layout_contiguous": [vp, ci, ci, ci, ci, ci, vp, vp, vp, vp, vp],
+            "dg_m_grouped_layout_masked": [vp, ci, ci, ci, ci, ci, vp, vp, vp, vp],
+            "dg_m_grouped_scatter_fp8_contiguous": [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp],
+            "dg_m_grouped_scatter_fp8_masked": [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, vp],
+            "dg_k_grouped_scatter_fp8": [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp],
+            "dg_m_grouped_gather": [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp],
+            "dg_m_grouped_gather_weight_grad": [vp, vp, vp, vp, ci, ci, ci, ci, vp],
+            "dg_lora_bf16_nt": [vp, ci, vp, vp, vp, vp, vp, ci, vp, ci, ci, ci, ci, ci, ci, vp],
+        }.items():
+            getattr(lib, name).argtypes = types
+            getattr(lib, name).restype = ci
         lib.dg_choose_config.argtypes = [ci, ci, ci, ci, ci, ci, ci, ci, ctypes.POINTER(ci), ctypes.POINTER(ci)]
         lib.dg_choose_config.restype = ci
         lib.dg_bind_stream_workspace.argtypes = [vp, vp, ctypes.c_size_t]
@@ -335,3 +362,192 @@ def dg_m_grouped_fp8_fp4_gemm_nt_masked(a, sfa, b, sfb, c, d, masked_m, expected
             max_m, N, K, G, _ptr(masked_m, "masked_m", _I32, (G,)), int(expected_m))
     _on_device(a=a, sfa=sfa, b=b, sfb=sfb, c=c, d=d, masked_m=masked_m)
     _check("dg_m_grouped_fp8_fp4_gemm_nt_masked", load().dg_m_grouped_fp8_fp4_gemm_nt_masked(*args, _stream(stream)))
+
+
+# ---- the operators around the products -------------------------------------
+_LOGITS = (torch.float32, torch.bfloat16)
+_BF16 = (torch.bfloat16,)
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _run(fn, tensors, args, stream):
+    """Checks that every tensor (None left out) lives on the current device, then makes the call."""
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != here:
+            _on_device(**{name: t})
+    _check(fn, getattr(load(), fn)(*args, _stream(stream)))
+
+
+def _score(score):
+    if score not in SCORES:
+        raise ValueError(f"score is {score!r}; expected one of {sorted(SCORES)}")
+    return SCORES[score]
+
+
+def _rank(t, name, dims):
+    """Whether t is a tensor of that many dimensions: sizes are read from it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() not in dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {' or '.join(map(str, dims))} dimensions")
+    return t.shape
+
+
+def dg_route_topk(logits, bias, topk_ids, topk_weights, score="softmax", num_groups=1, topk_groups=1, group_top=1,
+                  renormalize=True, scale=1.0, stream=None) -> None:
+    """Chooses each token's experts: topk_ids int32 and topk_weights fp32 [T][top_k] from logits [T][E]
+    (fp32 or bf16) and an optional fp32 bias [E] that steers the choice only."""
+    T, E = _rank(logits, "logits", (2,))
+    k = _rank(topk_ids, "topk_ids", (2,))[1]
+    args = (_ptr(logits, "logits", _LOGITS, None), 0 if logits.dtype == torch.float32 else 1,
+            _ptr(bias, "bias", _F32, (E,), True), _ptr(topk_ids, "topk_ids", _I32, (T, k)),
+            _ptr(topk_weights, "topk_weights", _F32, (T, k)), T, E, k, _score(score), int(num_groups),
+            int(topk_groups), int(group_top), 1 if renormalize else 0, float(scale))
+    _run("dg_route_topk", dict(logits=logits, bias=bias, topk_ids=topk_ids, topk_weights=topk_weights), args, stream)
+
+
+def dg_route_topk_backward(logits, topk_ids, grad_weights, grad_logits, score="softmax", renormalize=True, scale=1.0,
+                           stream=None) -> None:
+    """grad_logits [T][E] (of the logits' type) from the gradient of the forward call's weights [T][top_k]."""
+    T, E = _rank(logits, "logits", (2,))
+    k = _rank(topk_ids, "topk_ids", (2,))[1]
+    args = (_ptr(logits, "logits", _LOGITS, None), 0 if logits.dtype == torch.float32 else 1,
+            _ptr(topk_ids, "topk_ids", _I32, (T, k)), _ptr(grad_weights, "grad_weights", _F32, (T, k)),
+            _ptr(grad_logits, "grad_logits", (logits.dtype,), (T, E)), T, E, k, _score(score),
+            1 if renormalize else 0, float(scale))
+    _run("dg_route_topk_backward", dict(logits=logits, topk_ids=topk_ids, grad_weights=grad_weights,
+                                        grad_logits=grad_logits), args, stream)
+
+
+def dg_m_grouped_rows_bound(choices, num_groups) -> int:
+    """The most rows the contiguous layout of `choices` choices over num_groups experts can need."""
+    rows = load().dg_m_grouped_rows_bound(int(choices), int(num_groups))
+    if rows < 0:
+        raise ValueError(f"no row bound for {choices} choices over {num_groups} groups")
+    return rows
+
+
+def dg_m_grouped_layout_contiguous(topk_ids, first_expert, grouped_layout, row_of, slot_of, counts,
+                                   stream=None) -> None:
+    """Rows for the contiguous products from topk_ids int32 [T][top_k]: grouped_layout and slot_of int32 [M],
+    row_of int32 [T][top_k], counts int32 [num_groups]."""
+    T, k = _rank(topk_ids, "topk_ids", (2,))
+    M, G = _rank(grouped_layout, "grouped_layout", (1,))[0], _rank(counts, "counts", (1,))[0]
+    args = (_ptr(topk_ids, "topk_ids", _I32, None), T, k, int(first_expert), G, M,
+            _ptr(grouped_layout, "grouped_layout", _I32, None), _ptr(row_of, "row_of", _I32, (T, k)),
+            _ptr(slot_of, "slot_of", _I32, (M,)), _ptr(counts, "counts", _I32, None))
+    _run("dg_m_grouped_layout_contiguous", dict(topk_ids=topk_ids, grouped_layout=grouped_layout, row_of=row_of,
+                                                slot_of=slot_of, counts=counts), args, stream)
+
+
+def dg_m_grouped_layout_masked(topk_ids, first_expert, masked_m, row_of, slot_of, stream=None) -> None:
+    """Rows for the masked products: masked_m int32 [num_groups], row_of int32 [T][top_k],
+    slot_of int32 [num_groups][max_m]."""
+    T, k = _rank(topk_ids, "topk_ids", (2,))
+    G, m = _rank(slot_of, "slot_of", (2,))
+    args = (_ptr(topk_ids, "topk_ids", _I32, None), T, k, int(first_expert), G, m,
+            _ptr(masked_m, "masked_m", _I32, (G,)), _ptr(row_of, "row_of", _I32, (T, k)),
+            _ptr(slot_of, "slot_of", _I32, None))
+    _run("dg_m_grouped_layout_masked", dict(topk_ids=topk_ids, masked_m=masked_m, row_of=row_of, slot_of=slot_of),
+         args, stream)
+
+
+def dg_m_grouped_scatter_fp8_contiguous(x, weights, row_of, slot_of, a, sfa, pow2_scales=False, stream=None) -> None:
+    """The tokens' rows x bf16 [T][K], times weights fp32 [T][top_k] if given, quantised into
+    a [M][K] (e4m3 codes) and sfa fp32 [K/128][M] at the rows row_of / slot_of."""
+    T, K = _rank(x, "x", (2,))
+    k = _rank(row_of, "row_of", (2,))[1]
+    M = _rank(a, "a", (2,))[0]
+    args = (_ptr(x, "x", _BF16, None), _ptr(weights, "weights", _F32, (T, k), True),
+            _ptr(row_of, "row_of", _I32, (T, k)), _ptr(slot_of, "slot_of", _I32, (M,)),
+            _ptr(a, "a", _CODE_DTYPES, (M, K)), _ptr(sfa, "sfa", _F32, _sh(_kb(K), M)), T, k, M, K,
+            1 if pow2_scales else 0)
+    _run("dg_m_grouped_scatter_fp8_contiguous", dict(x=x, weights=weights, row_of=row_of, slot_of=slot_of, a=a,
+                                                     sfa=sfa), args, stream)
+
+
+def dg_m_grouped_scatter_fp8_masked(x, weights, row_of, slot_of, a, sfa, pow2_scales=False, stream=None) -> None:
+    """As the contiguous form, into a [G][max_m][K] and sfa fp32 [G][K/128][max_m]; slot_of [G][max_m]."""
+    T, K = _rank(x, "x", (2,))
+    k = _rank(row_of, "row_of", (2,))[1]
+    G, m, _ = _rank(a, "a", (3,))
+    args = (_ptr(x, "x", _BF16, None), _ptr(weights, "weights", _F32, (T, k), True),
+            _ptr(row_of, "row_of", _I32, (T, k)), _ptr(slot_of, "slot_of", _I32, (G, m)),
+            _ptr(a, "a", _CODE_DTYPES, (G, m, K)), _ptr(sfa, "sfa", _F32, _sh(G, _kb(K), m)), T, k, G, m, K,
+            1 if pow2_scales else 0)
+    _run("dg_m_grouped_scatter_fp8_masked", dict(x=x, weights=weights, row_of=row_of, slot_of=slot_of, a=a, sfa=sfa),
+         args, stream)
+
+
+def dg_k_grouped_scatter_fp8(x, weights, slot_of, top_k, a, sfa, pow2_scales=False, stream=None) -> None:
+    """The rows x bf16 [T][N] (times weights fp32 [T][top_k]) as a K-grouped operand: a [K][N] codes,
+    sfa fp32 [K/128][N], zeros in rows without a choice; slot_of int32 [K]."""
+    T, N = _rank(x, "x", (2,))
+    K = _rank(a, "a", (2,))[0]
+    k = int(top_k)
+    args = (_ptr(x, "x", _BF16, None), _ptr(weights, "weights", _F32, (T, k), True),
+            _ptr(slot_of, "slot_of", _I32, (K,)), _ptr(a, "a", _CODE_DTYPES, (K, N)),
+            _ptr(sfa, "sfa", _F32, _sh(_kb(K), N)), T, k, K, N, 1 if pow2_scales else 0)
+    _run("dg_k_grouped_scatter_fp8", dict(x=x, weights=weights, slot_of=slot_of, a=a, sfa=sfa), args, stream)
+
+
+def _rows2(rows):
+    """(M, N) of the experts' rows, [M][N] or the masked form's [G][max_m][N]."""
+    s = _rank(rows, "rows", (2, 3))
+    return (s[0], s[1]) if len(s) == 2 else (s[0] * s[1], s[2])
+
+
+def dg_m_grouped_gather(rows, row_of, weights, c, d, stream=None) -> None:
+    """d[t] = bf16(c[t] + sum_j weights[t][j] * rows[row_of[t][j]]): rows bf16 [M][N] or [G][max_m][N],
+    row_of int32 and weights fp32 (or None) [T][top_k], c (or None) and d bf16 [T][N]."""
+    M, N = _rows2(rows)
+    T, k = _rank(row_of, "row_of", (2,))
+    args = (_ptr(rows, "rows", _BF16, None), _ptr(row_of, "row_of", _I32, None),
+            _ptr(weights, "weights", _F32, (T, k), True), _ptr(c, "c", _BF16, (T, N), True),
+            _ptr(d, "d", _BF16, (T, N)), T, k, M, N)
+    _run("dg_m_grouped_gather", dict(rows=rows, row_of=row_of, weights=weights, c=c, d=d), args, stream)
+
+
+def dg_m_grouped_gather_weight_grad(rows, row_of, grad_d, grad_weights, stream=None) -> None:
+    """grad_weights[t][j] = grad_d[t] . rows[row_of[t][j]]: grad_d bf16 [T][N], grad_weights fp32 [T][top_k]."""
+    M, N = _rows2(rows)
+    T, k = _rank(row_of, "row_of", (2,))
+    args = (_ptr(rows, "rows", _BF16, None), _ptr(row_of, "row_of", _I32, None),
+            _ptr(grad_d, "grad_d", _BF16, (T, N)), _ptr(grad_weights, "grad_weights", _F32, (T, k)), T, k, M, N)
+    _run("dg_m_grouped_gather_weight_grad", dict(rows=rows, row_of=row_of, grad_d=grad_d, grad_weights=grad_weights),
+         args, stream)
+
+
+def _strided(t, name, shape, allow_none=False):
+    """(address, row stride) of a bf16 matrix whose rows are contiguous and may lie apart (a column slice)."""
+    if t is None and allow_none:
+        return None, shape[1]
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _BF16:
+        raise TypeError(f"{name} has dtype {t.dtype}; expected one of {_BF16}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    if (shape[1] > 1 and t.stride(1) != 1) or ld < shape[1]:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    if ld >= 1 << 31:
+        raise ValueError(f"{name} has rows {ld} elements apart; at most 2^31 - 1")
+    return t.data_ptr(), ld
+
+
+def dg_lora_bf16_nt(x, a, b, scales, adapter_ids, c, d, stream=None) -> None:
+    """d[t] = bf16(c[t] + scales[i] * b[i] . (a[i] . x[t])), i = adapter_ids[t]: x bf16 [T][K],
+    a bf16 [L][R][K], b bf16 [L][N][R], scales fp32 [L] or None, adapter_ids int32 [T], c (or None) and
+    d bf16 [T][N].  The rows of x, c and d may lie apart."""
+    T, K = _rank(x, "x", (2,))
+    L, R, _ = _rank(a, "a", (3,))
+    N = _rank(d, "d", (2,))[1]
+    px, ldx = _strided(x, "x", (T, K))
+    pc, ldc = _strided(c, "c", (T, N), True)
+    pd, ldd = _strided(d, "d", (T, N))
+    args = (px, ldx, _ptr(a, "a", _BF16, (L, R, K)), _ptr(b, "b", _BF16, (L, N, R)),
+            _ptr(scales, "scales", _F32, (L,), True), _ptr(adapter_ids, "adapter_ids", _I32, (T,)), pc, ldc, pd, ldd,
+            T, N, K, R, L)
+    _run("dg_lora_bf16_nt", dict(x=x, a=a, b=b, scales=scales, adapter_ids=adapter_ids, c=c, d=d), args, stream)

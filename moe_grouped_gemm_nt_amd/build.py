@@ -23,6 +23,9 @@ SOURCES = {
     "fp8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "fp8_gemm_e8m0.hip": [],
     "dg_api.hip": [],
+    "route.hip": [],
+    "expert_rows.hip": [],
+    "lora.hip": [],
 }
 
 # packed fp32 VALU forms are disabled on purpose: the kernels issue one fp32

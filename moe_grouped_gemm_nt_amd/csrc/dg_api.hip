@@ -37,26 +37,32 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "../../include/dg.h"
+#include "dg_host.h"
 #include "dg_internal.h"
 
 namespace {
+// The message of the last failure on this host thread.  A fixed buffer: no
+// allocation, so no exception can leave an entry point from here.
+thread_local char g_err[512];
+}  // namespace
 
-thread_local std::string g_err;
-
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace dg {
 int fail(int status, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
   va_end(ap);
-  g_err = buf;
   return status;
 }
+}  // namespace dg
+
+namespace {
+
+using dg::aligned;
+using dg::fail;
 
 constexpr int kMaxDevices = 64;
 constexpr size_t kWorkspaceBytes = size_t(64) << 20;    // split-K partial tiles
@@ -117,8 +123,6 @@ int get_device_state(DeviceState** out) {
   *out = &st;
   return DG_OK;
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_common(const void* a, const float* sfa, const void* b, const float* sfb, const void* c,
                  void* d, int M, int N, int K) {
@@ -532,7 +536,9 @@ bool find_binding(int dev, hipStream_t stream, Binding* out) {
   return false;
 }
 
-int launch(int mode, dg::Params& p, int rows_hint, hipStream_t stream) {
+// The device state and scratch memory of a call on `stream`: the device's
+// shared ones, or the stream's own workspace where one is bound.
+int resources_of(hipStream_t stream, Resources* out) {
   DeviceState* st = nullptr;
   int s = get_device_state(&st);
   if (s != DG_OK) return s;
@@ -548,10 +554,28 @@ int launch(int mode, dg::Params& p, int rows_hint, hipStream_t stream) {
     r.workspace = reinterpret_cast<float*>(b.ptr + ctl);
     r.ws_bytes = b.bytes - ctl;
   }
+  *out = r;
+  return DG_OK;
+}
+
+int launch(int mode, dg::Params& p, int rows_hint, hipStream_t stream) {
+  Resources r;
+  int s = resources_of(stream, &r);
+  if (s != DG_OK) return s;
   return launch_with(mode, p, rows_hint, stream, r);
 }
 
 }  // namespace
+
+namespace dg {
+int call_scratch(hipStream_t stream, Scratch* out) {
+  Resources r;
+  int s = resources_of(stream, &r);
+  if (s != DG_OK) return s;
+  *out = Scratch{r.num_cus, reinterpret_cast<uint8_t*>(r.workspace), r.ws_bytes};
+  return DG_OK;
+}
+}  // namespace dg
 
 extern "C" int dg_fp8_gemm_nt(const void* a, const float* sfa, const void* b, const float* sfb,
                               const void* c, void* d, int M, int N, int K, void* stream) {
@@ -919,6 +943,6 @@ extern "C" int dg_init(void) {
   return get_device_state(&st);
 }
 
-extern "C" const char* dg_last_error(void) { return g_err.c_str(); }
+extern "C" const char* dg_last_error(void) { return g_err; }
 
 extern "C" int dg_version(void) { return 100; }

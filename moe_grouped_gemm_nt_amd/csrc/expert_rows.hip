@@ -1,0 +1,559 @@
+// The tokens' rows out to the experts and back (include/dg.h): the layouts of
+// the grouped products, the quantising scatter into their A operands, and the
+// weighted gather of their results with the gradient of its weights.
+#include "expert_rows.h"
+
+#include <climits>
+
+#include "../../include/dg.h"
+#include "dg_host.h"
+
+namespace dg {
+namespace {
+
+// ============================================================================
+// layout
+// ============================================================================
+// A stable counting sort by group.  The choices are cut into chunks, one
+// workgroup each, and a chunk into one run per wave.  A choice's row is
+//   start[g] + (choices of g in earlier chunks) + (in earlier waves of the
+//   chunk) + (earlier in the wave's run),
+// the last from ballots over the bits of g, 64 choices at a time.
+constexpr int LT = 512;                  // threads per workgroup
+constexpr int LW = LT / 64;
+constexpr int kChunkLeast = 2048;        // choices per chunk before more workgroups are used
+constexpr int kChunksMost = 64;
+
+__device__ __forceinline__ int group_of(const LayoutParams& p, int i) {
+  const long long g = (long long)p.ids[i] - p.first;
+  return g >= 0 && g < p.groups ? (int)g : -1;
+}
+
+// counts[chunk][g] of each chunk
+__global__ __launch_bounds__(LT) void layout_count_kernel(LayoutParams p, int chunk, int32_t* counts) {
+  extern __shared__ int32_t lds[];
+  for (int g = threadIdx.x; g < p.groups; g += LT) lds[g] = 0;
+  __syncthreads();
+  const int begin = blockIdx.x * chunk, end = min(p.n, begin + chunk);
+  for (int i = begin + (int)threadIdx.x; i < end; i += LT) {
+    const int g = group_of(p, i);
+    if (g >= 0) atomicAdd(&lds[g], 1);
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < p.groups; g += LT) counts[(size_t)blockIdx.x * p.groups + g] = lds[g];
+}
+
+// Places one chunk's choices; every workgroup also fills its share of the
+// row-indexed outputs (layout, and slot_of where a row has no choice).
+__global__ __launch_bounds__(LT) void layout_place_kernel(LayoutParams p, int chunk, const int32_t* counts) {
+  extern __shared__ int32_t lds[];
+  const int G = p.groups;
+  int32_t* base = lds;                   // [LW][G]: next row of group g in wave w's run
+  int32_t* total = lds + LW * G;         // [G]: choices of group g
+  int32_t* start = total + G;            // [G + 1]: first row of group g
+  int32_t* prev = start + G + 1;         // [G]: choices of group g in earlier chunks
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int begin = min(p.n, (int)blockIdx.x * chunk), end = min(p.n, begin + chunk);
+  const int run = (end - begin + LW * 64 - 1) / (LW * 64) * 64;      // choices per wave
+  const int wb = min(end, begin + wave * run), we = min(end, wb + run);
+  for (int i = tid; i < (LW + 1) * G; i += LT) lds[i] = 0;
+  for (int g = tid; g < G; g += LT) prev[g] = 0;
+  __syncthreads();
+  for (int i = wb + lane; i < we; i += 64) {
+    const int g = group_of(p, i);
+    if (g >= 0) atomicAdd(&base[wave * G + g], 1);
+  }
+  if (counts) {                          // more than one chunk: all chunks' counts
+    const int chunks = gridDim.x;
+    for (int i = tid; i < chunks * G; i += LT) {
+      const int g = i % G, v = counts[i];
+      if (v == 0) continue;
+      atomicAdd(&total[g], v);
+      if (i / G < (int)blockIdx.x) atomicAdd(&prev[g], v);
+    }
+  }
+  __syncthreads();
+  if (!counts)
+    for (int g = tid; g < G; g += LT) {
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < LW; ++w) n += base[w * G + g];
+      total[g] = n;
+    }
+  __syncthreads();
+  // segment starts: an exclusive scan by the first wave (saturating: a row beyond
+  // INT_MAX is beyond p.rows too)
+  if (wave == 0) {
+    long long carry = 0;
+    for (int g0 = 0; g0 < G; g0 += 64) {
+      const int g = g0 + lane;
+      long long span = 0;
+      if (g < G) span = p.align ? ((long long)total[g] + p.align - 1) / p.align * p.align : p.max_m;
+      long long incl = span;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const long long up = __shfl_up(incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (g < G) start[g] = (int)min(carry + incl - span, (long long)INT_MAX);
+      carry += __shfl(incl, 63);
+    }
+    if (lane == 0) start[G] = (int)min(carry, (long long)INT_MAX);
+  }
+  __syncthreads();
+  for (int g = tid; g < G; g += LT) {    // counts in earlier waves, relative to the segment's start
+    int n = prev[g];
+#pragma unroll
+    for (int w = 0; w < LW; ++w) {
+      const int c = base[w * G + g];
+      base[w * G + g] = n;
+      n += c;
+    }
+    if (blockIdx.x == 0 && p.counts) p.counts[g] = p.align ? total[g] : min(total[g], p.max_m);
+  }
+  __syncthreads();
+  const int bits = 32 - __clz(G);        // ids 0..G-1, and G for a choice without a group
+  for (int i0 = wb; i0 < we; i0 += 64) {
+    const int i = i0 + lane;
+    int g = i < we ? group_of(p, i) : -1;
+    const int key = g >= 0 ? g : G;
+    uint64_t same = ~0ull;               // lanes with this lane's group
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t m = __ballot((key >> b) & 1);
+      same &= (key >> b) & 1 ? m : ~m;
+    }
+    int rank = 0;
+    if (g >= 0) {
+      const int at = wave * G + g;
+      rank = base[at] + __popcll(same & ((1ull << lane) - 1));
+      // the group's last lane moves the run's counter on; the reads above are of
+      // the same wave and come first
+      __builtin_amdgcn_wave_barrier();
+      if ((same >> lane) == 1) base[at] = rank + 1;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (i < we) {
+      const long long row = g >= 0 ? (long long)start[g] + rank : -1;
+      const bool fits = g >= 0 && row < p.rows && (p.align || rank < p.max_m);
+      if (p.row_of) p.row_of[i] = fits ? (int)row : -1;
+      if (fits) p.slot_of[row] = i;
+    }
+  }
+  // row-indexed outputs
+  for (long long r = (long long)blockIdx.x * LT + tid; r < p.rows; r += (long long)gridDim.x * LT) {
+    int g, rank;
+    if (p.align) {
+      int lo = 0, hi = G;                // the last group that starts at or before r
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= r) lo = mid; else hi = mid;
+      }
+      g = lo;
+      rank = (int)(r - start[g]);
+    } else {
+      g = (int)(r / p.max_m);
+      rank = (int)(r - (long long)g * p.max_m);
+    }
+    const bool used = rank < total[g];
+    if (p.layout) p.layout[r] = used ? g : -1;
+    if (!used) p.slot_of[r] = -1;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_layout(const LayoutParams& p, void* scratch, size_t scratch_bytes, hipStream_t stream) {
+  int chunks = (int)((p.n + (long long)kChunkLeast - 1) / kChunkLeast);
+  chunks = chunks < 1 ? 1 : (chunks > kChunksMost ? kChunksMost : chunks);
+  while (chunks > 1 && (size_t)chunks * p.groups * sizeof(int32_t) > scratch_bytes) --chunks;
+  const int chunk = (int)((p.n + (long long)chunks - 1) / chunks);
+  int32_t* counts = chunks > 1 ? static_cast<int32_t*>(scratch) : nullptr;
+  if (chunks > 1) {
+    layout_count_kernel<<<chunks, LT, sizeof(int32_t) * p.groups, stream>>>(p, chunk, counts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  layout_place_kernel<<<chunks, LT, sizeof(int32_t) * ((LW + 3) * p.groups + 1), stream>>>(p, chunk, counts);
+  return hipGetLastError();
+}
+
+namespace {
+
+// ============================================================================
+// scatter: quantise the tokens' rows into the products' A operands
+// ============================================================================
+constexpr float kE4m3Max = 448.0f;
+constexpr float kLeastAmax = 0x1p-100f;
+
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float bf16_f32(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+
+// The scale of a block whose largest magnitude is amax (include/dg.h).
+__device__ __forceinline__ float scale_of(float amax, bool pow2) {
+  if (!(amax > 0.0f)) return 1.0f;
+  float sf = __fdiv_rn(fmaxf(amax, kLeastAmax), kE4m3Max);
+  if (pow2) {
+    const uint32_t u = __float_as_uint(sf);              // normal: at least 2^-100 / 448
+    sf = u >= 0x7F800000u ? sf : __uint_as_float((u + 0x7FFFFFu) & 0x7F800000u);
+  }
+  return sf;
+}
+
+// Four e4m3 codes of clamp(v * inv) packed in an int; NaN stays NaN.
+__device__ __forceinline__ float clamp_e4m3(float v) {
+  const float c = fminf(fmaxf(v, -kE4m3Max), kE4m3Max);
+  return v == v ? c : v;
+}
+__device__ __forceinline__ int pack_e4m3(float a, float b, float c, float d) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(a), clamp_e4m3(b), 0, false);
+  return __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(c), clamp_e4m3(d), r, true);
+}
+
+struct ScatterParams {
+  const uint16_t* x;
+  const float* weights;
+  const int32_t* row_of;
+  const int32_t* slot_of;
+  uint8_t* a;
+  float* sfa;
+  int T, top_k;
+  int rows;                // all rows: M, or G * max_m
+  int rows_per_group;      // sfa is [rows / rows_per_group][K/128][rows_per_group]
+  int K;
+  int pow2;
+};
+
+// One workgroup per row, 16 lanes per block of 128 values.
+__global__ __launch_bounds__(256) void scatter_kernel(ScatterParams p) {
+  const int row = blockIdx.x;
+  const int slot = p.slot_of[row];
+  if (slot < 0 || slot >= (long long)p.T * p.top_k) return;
+  const uint16_t* x = p.x + (size_t)(slot / p.top_k) * p.K;
+  const float w = p.weights ? p.weights[slot] : 1.0f;
+  const int KB = p.K / 128;
+  float* sfa = p.sfa + (size_t)(row / p.rows_per_group) * KB * p.rows_per_group + row % p.rows_per_group;
+  for (int i = threadIdx.x; i < KB * 16; i += 256) {
+    const u16x8 h = *reinterpret_cast<const u16x8*>(x + 8 * i);
+    float v[8], amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = __fmul_rn(w, bf16_f32(h[j]));
+      amax = fmaxf(amax, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+    const float sf = scale_of(amax, p.pow2);
+    const float inv = __fdiv_rn(1.0f, sf);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
+    int2 q;
+    q.x = pack_e4m3(v[0], v[1], v[2], v[3]);
+    q.y = pack_e4m3(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<int2*>(p.a + (size_t)row * p.K + 8 * i) = q;
+    if ((i & 15) == 0) sfa[(size_t)(i >> 4) * p.rows_per_group] = sf;
+  }
+}
+
+struct KScatterParams {
+  const uint16_t* x;
+  const float* weights;
+  const int32_t* slot_of;
+  uint8_t* a;
+  float* sfa;
+  int T, top_k;
+  int K, N;                // K rows of N columns
+  int pow2;
+};
+
+// One workgroup per 128 rows x 128 columns: 16 threads across (8 columns each),
+// 16 rows in flight, 8 rows per thread.
+__global__ __launch_bounds__(256) void kscatter_kernel(KScatterParams p) {
+  __shared__ float lds[16][128];
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int row0 = blockIdx.y * 128;
+  const int col = blockIdx.x * 128 + tx * 8;
+  const bool in = col < p.N;               // N % 16 == 0: whole 8-column pieces
+  float v[8][8], amax[8] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int slot = p.slot_of[row0 + ty + 16 * i];
+    const bool live = in && slot >= 0 && slot < (long long)p.T * p.top_k;
+    u16x8 h = {};
+    float w = 1.0f;
+    if (live) {
+      h = *reinterpret_cast<const u16x8*>(p.x + (size_t)(slot / p.top_k) * p.N + col);
+      if (p.weights) w = p.weights[slot];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[i][j] = live ? __fmul_rn(w, bf16_f32(h[j])) : 0.0f;
+      amax[j] = fmaxf(amax[j], fabsf(v[i][j]));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) lds[ty][tx * 8 + j] = amax[j];
+  __syncthreads();
+  float inv[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float m = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) m = fmaxf(m, lds[r][tx * 8 + j]);
+    const float sf = scale_of(m, p.pow2);
+    inv[j] = __fdiv_rn(1.0f, sf);
+    if (in && ty == 0) p.sfa[(size_t)blockIdx.y * p.N + col + j] = sf;
+  }
+  if (!in) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], inv[j]);
+    int2 q;
+    q.x = pack_e4m3(v[i][0], v[i][1], v[i][2], v[i][3]);
+    q.y = pack_e4m3(v[i][4], v[i][5], v[i][6], v[i][7]);
+    *reinterpret_cast<int2*>(p.a + (size_t)(row0 + ty + 16 * i) * p.N + col) = q;
+  }
+}
+
+// ============================================================================
+// gather: the experts' rows back to the tokens
+// ============================================================================
+constexpr int kMaxTopK = 64;
+
+struct GatherParams {
+  const uint16_t* rows;
+  const int32_t* row_of;
+  const float* weights;
+  const uint16_t* c;
+  uint16_t* d;
+  const uint16_t* grad_d;
+  float* grad_weights;
+  int T, top_k, M, N;
+};
+
+__device__ __forceinline__ uint16_t f32_bf16(float x) {
+  __bf16 h = static_cast<__bf16>(x);
+  return __builtin_bit_cast(uint16_t, h);
+}
+
+__global__ __launch_bounds__(256) void gather_kernel(GatherParams p) {
+  const int t = blockIdx.x;
+  const int32_t* at = p.row_of + (size_t)t * p.top_k;
+  for (int n = threadIdx.x; n < p.N; n += 256) {
+    float sum = p.c ? bf16_f32(p.c[(size_t)t * p.N + n]) : 0.0f;
+    for (int j = 0; j < p.top_k; ++j) {
+      const int r = at[j];
+      if (r < 0 || r >= p.M) continue;
+      const float v = bf16_f32(p.rows[(size_t)r * p.N + n]);
+      sum = p.weights ? fmaf(p.weights[(size_t)t * p.top_k + j], v, sum) : sum + v;
+    }
+    p.d[(size_t)t * p.N + n] = f32_bf16(sum);
+  }
+}
+
+// One workgroup per choice.
+__global__ __launch_bounds__(256) void gather_weight_grad_kernel(GatherParams p) {
+  __shared__ float part[4];
+  const size_t i = blockIdx.x;
+  const int r = p.row_of[i];
+  float sum = 0.0f;
+  if (r >= 0 && r < p.M) {
+    const uint16_t* g = p.grad_d + (i / p.top_k) * p.N;
+    const uint16_t* v = p.rows + (size_t)r * p.N;
+    for (int n = threadIdx.x; n < p.N; n += 256) sum = fmaf(bf16_f32(g[n]), bf16_f32(v[n]), sum);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) p.grad_weights[i] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+int launched() {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? DG_OK : fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+}
+
+// ---- argument checks shared by the entry points ------------------------------
+constexpr long long kMaxChoices = 1LL << 30;
+
+int check_choices(int T, int top_k) {
+  if (T < 0 || top_k < 1) return fail(DG_ERR_INVALID_ARG, "T=%d must not be negative and top_k=%d at least 1", T, top_k);
+  if ((long long)T * top_k > kMaxChoices)
+    return fail(DG_ERR_UNSUPPORTED, "T * top_k = %lld choices exceed 2^30", (long long)T * top_k);
+  return DG_OK;
+}
+
+int check_layout_call(const int32_t* ids, int T, int top_k, int num_groups, const int32_t* row_of,
+                      const int32_t* slot_of, long long rows) {
+  int s = check_choices(T, top_k);
+  if (s != DG_OK) return s;
+  if (num_groups < 1) return fail(DG_ERR_INVALID_ARG, "num_groups=%d must be at least 1", num_groups);
+  if (num_groups > kMaxLayoutGroups)
+    return fail(DG_ERR_UNSUPPORTED, "num_groups=%d exceeds %d", num_groups, kMaxLayoutGroups);
+  if (rows > INT_MAX) return fail(DG_ERR_UNSUPPORTED, "%lld rows exceed 2^31 - 1", rows);
+  if (T > 0 && (!ids || !row_of)) return fail(DG_ERR_INVALID_ARG, "topk_ids and row_of must not be NULL");
+  if (rows > 0 && !slot_of) return fail(DG_ERR_INVALID_ARG, "slot_of must not be NULL");
+  if (!aligned(ids, 4) || !aligned(row_of, 4) || !aligned(slot_of, 4))
+    return fail(DG_ERR_INVALID_ARG, "topk_ids, row_of and slot_of must be 4-byte aligned");
+  return DG_OK;
+}
+
+int run_layout(LayoutParams& p, void* stream) {
+  Scratch sc;
+  const int s = call_scratch(static_cast<hipStream_t>(stream), &sc);
+  if (s != DG_OK) return s;
+  const hipError_t e = launch_layout(p, sc.ptr, sc.bytes, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? DG_OK : fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+}
+
+int scatter(const void* x, const float* weights, const int32_t* row_of, const int32_t* slot_of, void* a, float* sfa,
+            int T, int top_k, long long rows, int rows_per_group, int K, int pow2, void* stream) {
+  int s = check_choices(T, top_k);
+  if (s != DG_OK) return s;
+  if (K < 0) return fail(DG_ERR_INVALID_ARG, "negative size (K=%d)", K);
+  if (K % 128 != 0) return fail(DG_ERR_INVALID_ARG, "K=%d is not a multiple of 128", K);
+  if (rows > INT_MAX) return fail(DG_ERR_UNSUPPORTED, "%lld rows exceed 2^31 - 1", rows);
+  if (T == 0 || rows == 0 || K == 0) return DG_OK;
+  if (!x || !row_of || !slot_of || !a || !sfa)
+    return fail(DG_ERR_INVALID_ARG, "x, row_of, slot_of, a and sfa must not be NULL");
+  if (!aligned(x, 16) || !aligned(a, 16)) return fail(DG_ERR_INVALID_ARG, "x and a must be 16-byte aligned");
+  if (!aligned(sfa, 4) || !aligned(weights, 4) || !aligned(row_of, 4) || !aligned(slot_of, 4))
+    return fail(DG_ERR_INVALID_ARG, "sfa, weights, row_of and slot_of must be 4-byte aligned");
+  ScatterParams p{static_cast<const uint16_t*>(x), weights, row_of, slot_of, static_cast<uint8_t*>(a), sfa, T, top_k,
+                  (int)rows, rows_per_group, K, pow2 != 0};
+  scatter_kernel<<<(int)rows, 256, 0, static_cast<hipStream_t>(stream)>>>(p);
+  return launched();
+}
+
+int check_gather(const void* rows, const int32_t* row_of, int T, int top_k, int M, int N) {
+  int s = check_choices(T, top_k);
+  if (s != DG_OK) return s;
+  if (M < 0 || N < 0) return fail(DG_ERR_INVALID_ARG, "negative size (M=%d N=%d)", M, N);
+  if (top_k > kMaxTopK) return fail(DG_ERR_UNSUPPORTED, "top_k=%d exceeds %d", top_k, kMaxTopK);
+  if (T > 0 && !row_of) return fail(DG_ERR_INVALID_ARG, "row_of must not be NULL");
+  if (T > 0 && M > 0 && N > 0 && !rows) return fail(DG_ERR_INVALID_ARG, "rows must not be NULL");
+  if (!aligned(rows, 2) || !aligned(row_of, 4))
+    return fail(DG_ERR_INVALID_ARG, "rows must be 2-byte and row_of 4-byte aligned");
+  return DG_OK;
+}
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" int dg_m_grouped_rows_bound(long long choices, int num_groups) {
+  if (choices < 0 || num_groups < 0) return -1;
+  const long long used = choices < num_groups ? choices : num_groups;
+  if (choices > INT_MAX) return -1;
+  const long long rows = (choices + 127 * used) / 128 * 128;
+  return rows > INT_MAX ? -1 : (int)rows;
+}
+
+extern "C" int dg_m_grouped_layout_contiguous(const int32_t* topk_ids, int T, int top_k, int first_expert,
+                                              int num_groups, int M, int32_t* grouped_layout, int32_t* row_of,
+                                              int32_t* slot_of, int32_t* counts, void* stream) {
+  int s = check_layout_call(topk_ids, T, top_k, num_groups, row_of, slot_of, M);
+  if (s != DG_OK) return s;
+  if (M < 0 || M % 128 != 0) return fail(DG_ERR_INVALID_ARG, "M=%d is not a non-negative multiple of 128", M);
+  if (M > 0 && !grouped_layout) return fail(DG_ERR_INVALID_ARG, "grouped_layout must not be NULL");
+  if (!aligned(grouped_layout, 4) || !aligned(counts, 4))
+    return fail(DG_ERR_INVALID_ARG, "grouped_layout and counts must be 4-byte aligned");
+  LayoutParams p{topk_ids, T * top_k, first_expert, num_groups, 128, 0, M, grouped_layout, row_of, slot_of, counts};
+  return run_layout(p, stream);
+}
+
+extern "C" int dg_m_grouped_layout_masked(const int32_t* topk_ids, int T, int top_k, int first_expert, int num_groups,
+                                          int max_m, int32_t* masked_m, int32_t* row_of, int32_t* slot_of,
+                                          void* stream) {
+  if (max_m < 0) return fail(DG_ERR_INVALID_ARG, "negative size (max_m=%d)", max_m);
+  int s = check_layout_call(topk_ids, T, top_k, num_groups, row_of, slot_of, (long long)num_groups * max_m);
+  if (s != DG_OK) return s;
+  if (!masked_m) return fail(DG_ERR_INVALID_ARG, "masked_m must not be NULL");
+  if (!aligned(masked_m, 4)) return fail(DG_ERR_INVALID_ARG, "masked_m must be 4-byte aligned");
+  LayoutParams p{topk_ids, T * top_k, first_expert, num_groups, 0, max_m, num_groups * max_m, nullptr, row_of,
+                 slot_of, masked_m};
+  return run_layout(p, stream);
+}
+
+extern "C" int dg_m_grouped_scatter_fp8_contiguous(const void* x, const float* weights, const int32_t* row_of,
+                                                   const int32_t* slot_of, void* a, float* sfa, int T, int top_k,
+                                                   int M, int K, int pow2_scales, void* stream) {
+  if (M < 0) return fail(DG_ERR_INVALID_ARG, "negative size (M=%d)", M);
+  return scatter(x, weights, row_of, slot_of, a, sfa, T, top_k, M, M, K, pow2_scales, stream);
+}
+
+extern "C" int dg_m_grouped_scatter_fp8_masked(const void* x, const float* weights, const int32_t* row_of,
+                                               const int32_t* slot_of, void* a, float* sfa, int T, int top_k,
+                                               int num_groups, int max_m, int K, int pow2_scales, void* stream) {
+  if (num_groups < 1) return fail(DG_ERR_INVALID_ARG, "num_groups=%d must be at least 1", num_groups);
+  if (max_m < 0) return fail(DG_ERR_INVALID_ARG, "negative size (max_m=%d)", max_m);
+  return scatter(x, weights, row_of, slot_of, a, sfa, T, top_k, (long long)num_groups * max_m, max_m, K, pow2_scales,
+                 stream);
+}
+
+extern "C" int dg_k_grouped_scatter_fp8(const void* x, const float* weights, const int32_t* slot_of, void* a,
+                                        float* sfa, int T, int top_k, int K, int N, int pow2_scales, void* stream) {
+  int s = check_choices(T, top_k);
+  if (s != DG_OK) return s;
+  if (K < 0 || N < 0) return fail(DG_ERR_INVALID_ARG, "negative size (K=%d N=%d)", K, N);
+  if (K % 128 != 0) return fail(DG_ERR_INVALID_ARG, "K=%d is not a multiple of 128", K);
+  if (N % 16 != 0) return fail(DG_ERR_UNSUPPORTED, "the K-grouped product needs N a multiple of 16 (N=%d)", N);
+  if (K == 0 || N == 0) return DG_OK;
+  if ((T > 0 && !x) || !slot_of || !a || !sfa)
+    return fail(DG_ERR_INVALID_ARG, "x, slot_of, a and sfa must not be NULL");
+  if (!aligned(x, 16) || !aligned(a, 16)) return fail(DG_ERR_INVALID_ARG, "x and a must be 16-byte aligned");
+  if (!aligned(sfa, 4) || !aligned(weights, 4) || !aligned(slot_of, 4))
+    return fail(DG_ERR_INVALID_ARG, "sfa, weights and slot_of must be 4-byte aligned");
+  if (K / 128 > 65535) return fail(DG_ERR_UNSUPPORTED, "K=%d exceeds %d rows", K, 65535 * 128);
+  KScatterParams p{static_cast<const uint16_t*>(x), weights, slot_of, static_cast<uint8_t*>(a), sfa, T, top_k, K, N,
+                   pow2_scales != 0};
+  kscatter_kernel<<<dim3((N + 127) / 128, K / 128), 256, 0, static_cast<hipStream_t>(stream)>>>(p);
+  return launched();
+}
+
+extern "C" int dg_m_grouped_gather(const void* rows, const int32_t* row_of, const float* weights, const void* c,
+                                   void* d, int T, int top_k, int M, int N, void* stream) {
+  int s = check_gather(rows, row_of, T, top_k, M, N);
+  if (s != DG_OK) return s;
+  if (T == 0 || N == 0) return DG_OK;
+  if (!d) return fail(DG_ERR_INVALID_ARG, "d must not be NULL");
+  if (!aligned(d, 2) || !aligned(c, 2) || !aligned(weights, 4))
+    return fail(DG_ERR_INVALID_ARG, "c and d must be 2-byte and weights 4-byte aligned");
+  GatherParams p{};
+  p.rows = static_cast<const uint16_t*>(rows);
+  p.row_of = row_of;
+  p.weights = weights;
+  p.c = static_cast<const uint16_t*>(c);
+  p.d = static_cast<uint16_t*>(d);
+  p.T = T;
+  p.top_k = top_k;
+  p.M = M;
+  p.N = N;
+  gather_kernel<<<T, 256, 0, static_cast<hipStream_t>(stream)>>>(p);
+  return launched();
+}
+
+extern "C" int dg_m_grouped_gather_weight_grad(const void* rows, const int32_t* row_of, const void* grad_d,
+                                               float* grad_weights, int T, int top_k, int M, int N, void* stream) {
+  int s = check_gather(rows, row_of, T, top_k, M, N);
+  if (s != DG_OK) return s;
+  if (T == 0) return DG_OK;
+  if ((N > 0 && !grad_d) || !grad_weights)
+    return fail(DG_ERR_INVALID_ARG, "grad_d and grad_weights must not be NULL");
+  if (!aligned(grad_d, 2) || !aligned(grad_weights, 4))
+    return fail(DG_ERR_INVALID_ARG, "grad_d must be 2-byte and grad_weights 4-byte aligned");
+  GatherParams p{};
+  p.rows = static_cast<const uint16_t*>(rows);
+  p.row_of = row_of;
+  p.grad_d = static_cast<const uint16_t*>(grad_d);
+  p.grad_weights = grad_weights;
+  p.T = T;
+  p.top_k = top_k;
+  p.M = M;
+  p.N = N;
+  gather_weight_grad_kernel<<<T * top_k, 256, 0, static_cast<hipStream_t>(stream)>>>(p);
+  return launched();
+}

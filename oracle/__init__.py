@@ -1,5 +1,6 @@
 """CPU oracle for the FP8 block-scaled GEMM (NT and the nn/tn/tt storages), its
-M-grouped MoE forms, the K-grouped TN form and the FP8 x FP4 GEMM.
+M-grouped MoE forms, the K-grouped TN form and the FP8 x FP4 GEMM; and
+(``around``) for the operators around them.
 
 TEST INFRASTRUCTURE ONLY.  Only the test suite, the smoke check and the
 benchmark's CPU-baseline leg may import this package.  The library's GPU path
@@ -8,6 +9,7 @@ never calls it and shares no code with it.
 The oracle is plain numpy in fp64.  See ``fp8_gemm`` for the definitions and
 the passages of the DeepGEMM pages each step follows.
 """
+from . import around  # noqa: F401
 from .fp8_gemm import (  # noqa: F401
     E4M3_VALUES,
     decode_e4m3,
