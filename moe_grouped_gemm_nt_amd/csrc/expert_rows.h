@@ -9,7 +9,7 @@
 
 namespace dg {
 
-constexpr int kMaxLayoutGroups = 1024;
+constexpr int kMaxLayoutGroups = 1024;   // (and one more with `others`)
 
 struct LayoutParams {
   const int32_t* ids;      // [n] group of each choice, counted from `first`
@@ -22,6 +22,7 @@ struct LayoutParams {
   int32_t* row_of;         // [n] row of each choice or -1, or nullptr
   int32_t* slot_of;        // [rows] choice of each row or -1
   int32_t* counts;         // [groups] or nullptr: choices per group (masked: at most max_m)
+  int others;              // nonzero: choices outside the first groups - 1 ids form the last group
 };
 
 // Enqueues the layout kernels; `scratch` may be too small for more than one

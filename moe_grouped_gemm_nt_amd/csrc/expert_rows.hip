@@ -26,7 +26,8 @@ constexpr int kChunksMost = 64;
 
 __device__ __forceinline__ int group_of(const LayoutParams& p, int i) {
   const long long g = (long long)p.ids[i] - p.first;
-  return g >= 0 && g < p.groups ? (int)g : -1;
+  const int last = p.others ? p.groups - 1 : -1;
+  return g >= 0 && g < p.groups - (p.others != 0) ? (int)g : last;
 }
 
 // counts[chunk][g] of each chunk
@@ -461,7 +462,7 @@ extern "C" int dg_m_grouped_layout_contiguous(const int32_t* topk_ids, int T, in
   if (M > 0 && !grouped_layout) return fail(DG_ERR_INVALID_ARG, "grouped_layout must not be NULL");
   if (!aligned(grouped_layout, 4) || !aligned(counts, 4))
     return fail(DG_ERR_INVALID_ARG, "grouped_layout and counts must be 4-byte aligned");
-  LayoutParams p{topk_ids, T * top_k, first_expert, num_groups, 128, 0, M, grouped_layout, row_of, slot_of, counts};
+  LayoutParams p{topk_ids, T * top_k, first_expert, num_groups, 128, 0, M, grouped_layout, row_of, slot_of, counts, 0};
   return run_layout(p, stream);
 }
 
@@ -474,7 +475,7 @@ extern "C" int dg_m_grouped_layout_masked(const int32_t* topk_ids, int T, int to
   if (!masked_m) return fail(DG_ERR_INVALID_ARG, "masked_m must not be NULL");
   if (!aligned(masked_m, 4)) return fail(DG_ERR_INVALID_ARG, "masked_m must be 4-byte aligned");
   LayoutParams p{topk_ids, T * top_k, first_expert, num_groups, 0, max_m, num_groups * max_m, nullptr, row_of,
-                 slot_of, masked_m};
+                 slot_of, masked_m, 0};
   return run_layout(p, stream);
 }
 
