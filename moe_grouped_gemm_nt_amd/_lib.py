@@ -139,6 +139,8 @@ def _ptr(t, name, dtypes, shape, allow_none=False):
         if allow_none:
             return None
         raise ValueError(f"{name} must not be None")
+    if type(t) is torch.Tensor and t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -371,12 +373,19 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 def _run(fn, tensors, args, stream):
-    """Checks that every tensor (None left out) lives on the current device, then makes the call."""
+    """Checks that every tensor (None left out) lives on the current device, then makes the call.
+    These calls take a few microseconds on the device, so the host side is kept as short."""
     here = torch.cuda.current_device() if torch.cuda.is_initialized() else None
-    for name, t in tensors.items():
+    for t in tensors.values():
         if t is not None and t.get_device() != here:
-            _on_device(**{name: t})
-    _check(fn, getattr(load(), fn)(*args, _stream(stream)))
+            _on_device(**tensors)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(here)
+    else:
+        stream = _stream(stream)
+    status = getattr(_lib or load(), fn)(*args, stream)
+    if status:
+        _check(fn, status)
 
 
 def _score(score):

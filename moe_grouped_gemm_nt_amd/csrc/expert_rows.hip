@@ -338,37 +338,105 @@ __device__ __forceinline__ uint16_t f32_bf16(float x) {
   return __builtin_bit_cast(uint16_t, h);
 }
 
-__global__ __launch_bounds__(256) void gather_kernel(GatherParams p) {
-  const int t = blockIdx.x;
-  const int32_t* at = p.row_of + (size_t)t * p.top_k;
-  for (int n = threadIdx.x; n < p.N; n += 256) {
-    float sum = p.c ? bf16_f32(p.c[(size_t)t * p.N + n]) : 0.0f;
-    for (int j = 0; j < p.top_k; ++j) {
-      const int r = at[j];
-      if (r < 0 || r >= p.M) continue;
-      const float v = bf16_f32(p.rows[(size_t)r * p.N + n]);
-      sum = p.weights ? fmaf(p.weights[(size_t)t * p.top_k + j], v, sum) : sum + v;
-    }
-    p.d[(size_t)t * p.N + n] = f32_bf16(sum);
-  }
+// Eight neighbouring bf16 at any 2-byte address (rows of an odd N start anywhere;
+// the hardware's 16-byte loads and stores take any alignment).
+typedef u16x8 u16x8_any __attribute__((aligned(2)));
+
+// Columns n..n+7 of a row, zeros beyond N.
+__device__ __forceinline__ u16x8 load_piece(const uint16_t* row, int n, int N) {
+  if (n + 8 <= N) return *reinterpret_cast<const u16x8_any*>(row + n);
+  u16x8 v = {};
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (n + e < N) v[e] = row[n + e];
+  return v;
 }
 
-// One workgroup per choice.
+constexpr int GJ = 8;                    // rows in flight per thread
+
+// One thread per token and eight columns; the token's rows and weights are the
+// same for the whole workgroup.  Bound by the rows' bytes: GJ 16-byte loads per
+// thread are in flight before the first is summed.
+__global__ __launch_bounds__(256) void gather_kernel(GatherParams p) {
+  const size_t t = blockIdx.x;
+  const int n = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+  if (n >= p.N) return;
+  const int32_t* __restrict__ at = p.row_of + t * p.top_k;
+  const float* __restrict__ w = p.weights ? p.weights + t * p.top_k : nullptr;
+  float sum[8] = {};
+  if (p.c) {
+    const u16x8 c = load_piece(p.c + t * p.N, n, p.N);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = bf16_f32(c[e]);
+  }
+  for (int j0 = 0; j0 < p.top_k; j0 += GJ) {
+    u16x8 v[GJ];
+    float wt[GJ];
+    bool has[GJ];
+#pragma unroll
+    for (int j = 0; j < GJ; ++j) {
+      const int r = j0 + j < p.top_k ? at[j0 + j] : -1;
+      has[j] = r >= 0 && r < p.M;
+      if (has[j]) {
+        v[j] = load_piece(p.rows + (size_t)r * p.N, n, p.N);
+        wt[j] = w ? w[j0 + j] : 1.0f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < GJ; ++j)
+      if (has[j])
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = fmaf(wt[j], bf16_f32(v[j][e]), sum[e]);
+  }
+  uint16_t* d = p.d + t * p.N + n;
+  u16x8 o;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = f32_bf16(sum[e]);
+  if (n + 8 <= p.N)
+    *reinterpret_cast<u16x8_any*>(d) = o;
+  else
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (n + e < p.N) d[e] = o[e];
+}
+
+// One workgroup per token and JG of its choices: a piece of grad_d is read once
+// for them all.
+template <int JG>
 __global__ __launch_bounds__(256) void gather_weight_grad_kernel(GatherParams p) {
-  __shared__ float part[4];
-  const size_t i = blockIdx.x;
-  const int r = p.row_of[i];
-  float sum = 0.0f;
-  if (r >= 0 && r < p.M) {
-    const uint16_t* g = p.grad_d + (i / p.top_k) * p.N;
-    const uint16_t* v = p.rows + (size_t)r * p.N;
-    for (int n = threadIdx.x; n < p.N; n += 256) sum = fmaf(bf16_f32(g[n]), bf16_f32(v[n]), sum);
+  __shared__ float part[4][JG];
+  const size_t t = blockIdx.x;
+  const int j0 = blockIdx.y * JG;
+  const uint16_t* g = p.grad_d + t * p.N;
+  const uint16_t* row[JG];
+#pragma unroll
+  for (int j = 0; j < JG; ++j) {
+    const int r = j0 + j < p.top_k ? p.row_of[t * p.top_k + j0 + j] : -1;
+    row[j] = r >= 0 && r < p.M ? p.rows + (size_t)r * p.N : nullptr;
+  }
+  float sum[JG] = {};
+  for (int n = threadIdx.x * 8; n < p.N; n += 256 * 8) {
+    const u16x8 gv = load_piece(g, n, p.N);
+    u16x8 v[JG];
+#pragma unroll
+    for (int j = 0; j < JG; ++j)
+      if (row[j]) v[j] = load_piece(row[j], n, p.N);
+#pragma unroll
+    for (int j = 0; j < JG; ++j)
+      if (row[j])
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[j] = fmaf(bf16_f32(gv[e]), bf16_f32(v[j][e]), sum[j]);
   }
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  for (int j = 0; j < JG; ++j) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum[j] += __shfl_xor(sum[j], o);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][j] = sum[j];
+  }
   __syncthreads();
-  if (threadIdx.x == 0) p.grad_weights[i] = (part[0] + part[1]) + (part[2] + part[3]);
+  const int j = threadIdx.x;
+  if (j < JG && j0 + j < p.top_k)
+    p.grad_weights[t * p.top_k + j0 + j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
 }
 
 int launched() {
@@ -378,6 +446,8 @@ int launched() {
 
 // ---- argument checks shared by the entry points ------------------------------
 constexpr long long kMaxChoices = 1LL << 30;
+constexpr int kMaxTokens = 1 << 23;      // one workgroup each, of at most 256 threads: a grid's thread count is 32 bits
+constexpr int kMaxColumns = 1 << 23;     // 512 to a workgroup
 
 int check_choices(int T, int top_k) {
   if (T < 0 || top_k < 1) return fail(DG_ERR_INVALID_ARG, "T=%d must not be negative and top_k=%d at least 1", T, top_k);
@@ -433,6 +503,8 @@ int check_gather(const void* rows, const int32_t* row_of, int T, int top_k, int 
   if (s != DG_OK) return s;
   if (M < 0 || N < 0) return fail(DG_ERR_INVALID_ARG, "negative size (M=%d N=%d)", M, N);
   if (top_k > kMaxTopK) return fail(DG_ERR_UNSUPPORTED, "top_k=%d exceeds %d", top_k, kMaxTopK);
+  if (T > kMaxTokens || N > kMaxColumns)
+    return fail(DG_ERR_UNSUPPORTED, "T=%d or N=%d exceeds %d tokens and %d columns", T, N, kMaxTokens, kMaxColumns);
   if (T > 0 && !row_of) return fail(DG_ERR_INVALID_ARG, "row_of must not be NULL");
   if (T > 0 && M > 0 && N > 0 && !rows) return fail(DG_ERR_INVALID_ARG, "rows must not be NULL");
   if (!aligned(rows, 2) || !aligned(row_of, 4))
@@ -533,7 +605,10 @@ extern "C" int dg_m_grouped_gather(const void* rows, const int32_t* row_of, cons
   p.top_k = top_k;
   p.M = M;
   p.N = N;
-  gather_kernel<<<T, 256, 0, static_cast<hipStream_t>(stream)>>>(p);
+  // 2048 columns per workgroup, or 512 where that would leave CUs without one
+  const int pieces = (int)((N + 7LL) / 8);
+  const int threads = (long long)T * ((pieces + 255) / 256) >= 512 ? 256 : 64;
+  gather_kernel<<<dim3(T, (pieces + threads - 1) / threads), threads, 0, static_cast<hipStream_t>(stream)>>>(p);
   return launched();
 }
 
@@ -555,6 +630,10 @@ extern "C" int dg_m_grouped_gather_weight_grad(const void* rows, const int32_t* 
   p.top_k = top_k;
   p.M = M;
   p.N = N;
-  gather_weight_grad_kernel<<<T * top_k, 256, 0, static_cast<hipStream_t>(stream)>>>(p);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (top_k <= 2 || T < 512)
+    gather_weight_grad_kernel<2><<<dim3(T, (top_k + 1) / 2), 256, 0, st>>>(p);
+  else
+    gather_weight_grad_kernel<8><<<dim3(T, (top_k + 7) / 8), 256, 0, st>>>(p);
   return launched();
 }
