@@ -4,6 +4,7 @@
 #include "expert_rows.h"
 
 #include <climits>
+#include <type_traits>
 
 #include "../../include/dg.h"
 #include "dg_host.h"
@@ -342,9 +343,12 @@ __device__ __forceinline__ uint16_t f32_bf16(float x) {
 // the hardware's 16-byte loads and stores take any alignment).
 typedef u16x8 u16x8_any __attribute__((aligned(2)));
 
-// Columns n..n+7 of a row, zeros beyond N.
+constexpr int GJ = 8;                    // rows in flight per thread
+
+// Columns n..n+7 of a row (WHOLE), or its columns from n up to N, then zeros.
+template <bool WHOLE>
 __device__ __forceinline__ u16x8 load_piece(const uint16_t* row, int n, int N) {
-  if (n + 8 <= N) return *reinterpret_cast<const u16x8_any*>(row + n);
+  if constexpr (WHOLE) return *reinterpret_cast<const u16x8_any*>(row + n);
   u16x8 v = {};
 #pragma unroll
   for (int e = 0; e < 7; ++e)
@@ -352,52 +356,60 @@ __device__ __forceinline__ u16x8 load_piece(const uint16_t* row, int n, int N) {
   return v;
 }
 
-constexpr int GJ = 8;                    // rows in flight per thread
-
-// One thread per token and eight columns; the token's rows and weights are the
-// same for the whole workgroup.  Bound by the rows' bytes: GJ 16-byte loads per
-// thread are in flight before the first is summed.
-__global__ __launch_bounds__(256) void gather_kernel(GatherParams p) {
-  const size_t t = blockIdx.x;
-  const int n = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
-  if (n >= p.N) return;
-  const int32_t* __restrict__ at = p.row_of + t * p.top_k;
-  const float* __restrict__ w = p.weights ? p.weights + t * p.top_k : nullptr;
+template <bool WHOLE>
+__device__ __forceinline__ void gather_piece(const GatherParams& p, size_t t, int n) {
   float sum[8] = {};
   if (p.c) {
-    const u16x8 c = load_piece(p.c + t * p.N, n, p.N);
+    const u16x8 c = load_piece<WHOLE>(p.c + t * p.N, n, p.N);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = bf16_f32(c[e]);
   }
   for (int j0 = 0; j0 < p.top_k; j0 += GJ) {
-    u16x8 v[GJ];
-    float wt[GJ];
-    bool has[GJ];
+    // the same for the workgroup: scalar loads, in flight together
+    int rs[GJ];
+    float ws[GJ];
 #pragma unroll
     for (int j = 0; j < GJ; ++j) {
-      const int r = j0 + j < p.top_k ? at[j0 + j] : -1;
-      has[j] = r >= 0 && r < p.M;
-      if (has[j]) {
-        v[j] = load_piece(p.rows + (size_t)r * p.N, n, p.N);
-        wt[j] = w ? w[j0 + j] : 1.0f;
-      }
+      const bool in = j0 + j < p.top_k;
+      const int r = p.row_of[t * p.top_k + (in ? j0 + j : 0)];
+      rs[j] = in && r >= 0 && r < p.M ? r : -1;
+      ws[j] = p.weights ? p.weights[t * p.top_k + (in ? j0 + j : 0)] : 1.0f;
     }
+    int some = -1;                       // a slot without a row loads another's again: no branch between the loads
+#pragma unroll
+    for (int j = 0; j < GJ; ++j) some = rs[j] >= 0 ? rs[j] : some;
+    if (some < 0) continue;
+    u16x8 v[GJ];
 #pragma unroll
     for (int j = 0; j < GJ; ++j)
-      if (has[j])
+      v[j] = load_piece<WHOLE>(p.rows + (size_t)(rs[j] >= 0 ? rs[j] : some) * p.N, n, p.N);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] = fmaf(wt[j], bf16_f32(v[j][e]), sum[e]);
+    for (int j = 0; j < GJ; ++j)
+      if (rs[j] >= 0)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = fmaf(ws[j], bf16_f32(v[j][e]), sum[e]);
   }
   uint16_t* d = p.d + t * p.N + n;
   u16x8 o;
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = f32_bf16(sum[e]);
-  if (n + 8 <= p.N)
+  if constexpr (WHOLE)
     *reinterpret_cast<u16x8_any*>(d) = o;
   else
 #pragma unroll
     for (int e = 0; e < 7; ++e)
       if (n + e < p.N) d[e] = o[e];
+}
+
+// One thread per token and eight columns; the token's rows and weights are the
+// same for the whole workgroup.  Bound by the rows' bytes: GJ 16-byte loads per
+// thread are in flight before the first is summed.
+__global__ __launch_bounds__(256) void gather_kernel(GatherParams p) {
+  const int n = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+  if (n + 8 <= p.N)
+    gather_piece<true>(p, blockIdx.x, n);
+  else if (n < p.N)
+    gather_piece<false>(p, blockIdx.x, n);
 }
 
 // One workgroup per token and JG of its choices: a piece of grad_d is read once
@@ -408,25 +420,33 @@ __global__ __launch_bounds__(256) void gather_weight_grad_kernel(GatherParams p)
   const size_t t = blockIdx.x;
   const int j0 = blockIdx.y * JG;
   const uint16_t* g = p.grad_d + t * p.N;
-  const uint16_t* row[JG];
+  int rs[JG], some = -1;
 #pragma unroll
   for (int j = 0; j < JG; ++j) {
-    const int r = j0 + j < p.top_k ? p.row_of[t * p.top_k + j0 + j] : -1;
-    row[j] = r >= 0 && r < p.M ? p.rows + (size_t)r * p.N : nullptr;
+    const bool in = j0 + j < p.top_k;
+    const int r = p.row_of[t * p.top_k + (in ? j0 + j : j0)];
+    rs[j] = in && r >= 0 && r < p.M ? r : -1;
+    some = rs[j] >= 0 ? rs[j] : some;
   }
+  const uint16_t* row[JG];               // a slot without a row reads another's again and keeps 0
+#pragma unroll
+  for (int j = 0; j < JG; ++j) row[j] = p.rows + (size_t)(rs[j] >= 0 ? rs[j] : some) * p.N;
   float sum[JG] = {};
-  for (int n = threadIdx.x * 8; n < p.N; n += 256 * 8) {
-    const u16x8 gv = load_piece(g, n, p.N);
+  auto add = [&](auto whole, int n) {
+    const u16x8 gv = load_piece<whole.value>(g, n, p.N);
     u16x8 v[JG];
 #pragma unroll
-    for (int j = 0; j < JG; ++j)
-      if (row[j]) v[j] = load_piece(row[j], n, p.N);
+    for (int j = 0; j < JG; ++j) v[j] = load_piece<whole.value>(row[j], n, p.N);
 #pragma unroll
     for (int j = 0; j < JG; ++j)
-      if (row[j])
+      if (rs[j] >= 0)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[j] = fmaf(bf16_f32(gv[e]), bf16_f32(v[j][e]), sum[j]);
-  }
+  };
+  int n = some >= 0 ? threadIdx.x * 8 : p.N;
+#pragma unroll 2
+  for (; n + 8 <= p.N; n += 256 * 8) add(std::true_type{}, n);
+  if (n < p.N) add(std::false_type{}, n);
 #pragma unroll
   for (int j = 0; j < JG; ++j) {
 #pragma unroll
