@@ -226,34 +226,80 @@ struct ScatterParams {
   int pow2;
 };
 
-// One workgroup per row, 16 lanes per block of 128 values.
+constexpr int SJ = 8;                    // rows a thread writes per turn; also lanes per block
+
+// One thread per sixteen values of a token, eight threads per block of 128: the
+// token is read and quantised once and stored to all its rows (without weights;
+// with them the products are quantised per row).  In each group of eight lanes,
+// lane i also works out and stores the scale of row i of the turn.
+template <bool WEIGHTED, bool MASKED>
 __global__ __launch_bounds__(256) void scatter_kernel(ScatterParams p) {
-  const int row = blockIdx.x;
-  const int slot = p.slot_of[row];
-  if (slot < 0 || slot >= (long long)p.T * p.top_k) return;
-  const uint16_t* x = p.x + (size_t)(slot / p.top_k) * p.K;
-  const float w = p.weights ? p.weights[slot] : 1.0f;
-  const int KB = p.K / 128;
-  float* sfa = p.sfa + (size_t)(row / p.rows_per_group) * KB * p.rows_per_group + row % p.rows_per_group;
-  for (int i = threadIdx.x; i < KB * 16; i += 256) {
-    const u16x8 h = *reinterpret_cast<const u16x8*>(x + 8 * i);
-    float v[8], amax = 0.0f;
+  const int per_token = p.K / 16;
+  const size_t total = (size_t)p.T * per_token;        // a multiple of 8
+  const int lane8 = threadIdx.x & 7;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
+    const int t = (int)(i / per_token);
+    const int k = (int)(i - (size_t)t * per_token) * 16;
+    const u16x8* x = reinterpret_cast<const u16x8*>(p.x + (size_t)t * p.K + k);
+    const u16x8 h0 = x[0], h1 = x[1];
+    float v[16], amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = __fmul_rn(w, bf16_f32(h[j]));
-      amax = fmaxf(amax, fabsf(v[j]));
+    for (int e = 0; e < 8; ++e) {
+      v[e] = bf16_f32(h0[e]);
+      v[8 + e] = bf16_f32(h1[e]);
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-    const float sf = scale_of(amax, p.pow2);
-    const float inv = __fdiv_rn(1.0f, sf);
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(v[e]));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
-    int2 q;
-    q.x = pack_e4m3(v[0], v[1], v[2], v[3]);
-    q.y = pack_e4m3(v[4], v[5], v[6], v[7]);
-    *reinterpret_cast<int2*>(p.a + (size_t)row * p.K + 8 * i) = q;
-    if ((i & 15) == 0) sfa[(size_t)(i >> 4) * p.rows_per_group] = sf;
+    for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+    int4 q;
+    float sf = 1.0f;
+    if constexpr (!WEIGHTED) {
+      sf = scale_of(amax, p.pow2);
+      const float inv = __fdiv_rn(1.0f, sf);
+      float u[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) u[e] = __fmul_rn(v[e], inv);
+      q = make_int4(pack_e4m3(u[0], u[1], u[2], u[3]), pack_e4m3(u[4], u[5], u[6], u[7]),
+                    pack_e4m3(u[8], u[9], u[10], u[11]), pack_e4m3(u[12], u[13], u[14], u[15]));
+    }
+    for (int j0 = 0; j0 < p.top_k; j0 += SJ) {
+      const int32_t* at = p.row_of + (size_t)t * p.top_k + j0;
+      const float* wt = WEIGHTED ? p.weights + (size_t)t * p.top_k + j0 : nullptr;
+      const int left = p.top_k - j0;
+      int rows[SJ];
+#pragma unroll
+      for (int j = 0; j < SJ; ++j) rows[j] = at[j < left ? j : 0];
+      const int mine = lane8 < left ? at[lane8] : -1;          // this lane's row of the scales
+      float inv = 0.0f;
+      if constexpr (WEIGHTED) {
+        // max |w x| = |w| max |x|, rounding included
+        sf = scale_of(__fmul_rn(fabsf(wt[lane8 < left ? lane8 : 0]), amax), p.pow2);
+        inv = __fdiv_rn(1.0f, sf);
+      }
+      if (mine >= 0 && mine < p.rows) {
+        const int KB = p.K / 128, kb = k / 128;
+        if constexpr (MASKED) {
+          const int g = mine / p.rows_per_group;
+          p.sfa[((size_t)g * KB + kb) * p.rows_per_group + (mine - g * p.rows_per_group)] = sf;
+        } else {
+          p.sfa[(size_t)kb * p.rows + mine] = sf;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < SJ; ++j) {
+        if (j >= left) break;
+        if constexpr (WEIGHTED) {
+          const float w = wt[j], f = __shfl(inv, j, 8);
+          float u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) u[e] = __fmul_rn(__fmul_rn(w, v[e]), f);
+          q = make_int4(pack_e4m3(u[0], u[1], u[2], u[3]), pack_e4m3(u[4], u[5], u[6], u[7]),
+                        pack_e4m3(u[8], u[9], u[10], u[11]), pack_e4m3(u[12], u[13], u[14], u[15]));
+        }
+        if (rows[j] >= 0 && rows[j] < p.rows) *reinterpret_cast<int4*>(p.a + (size_t)rows[j] * p.K + k) = q;
+      }
+    }
   }
 }
 
@@ -524,7 +570,13 @@ int scatter(const void* x, const float* weights, const int32_t* row_of, const in
     return fail(DG_ERR_INVALID_ARG, "sfa, weights, row_of and slot_of must be 4-byte aligned");
   ScatterParams p{static_cast<const uint16_t*>(x), weights, row_of, slot_of, static_cast<uint8_t*>(a), sfa, T, top_k,
                   (int)rows, rows_per_group, K, pow2 != 0};
-  scatter_kernel<<<(int)rows, 256, 0, static_cast<hipStream_t>(stream)>>>(p);
+  const long long wgs = ((long long)T * (K / 16) + 255) / 256;
+  const int grid = (int)(wgs < kMaxGrid ? wgs : kMaxGrid);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (rows_per_group != rows)
+    weights ? scatter_kernel<true, true><<<grid, 256, 0, st>>>(p) : scatter_kernel<false, true><<<grid, 256, 0, st>>>(p);
+  else
+    weights ? scatter_kernel<true, false><<<grid, 256, 0, st>>>(p) : scatter_kernel<false, false><<<grid, 256, 0, st>>>(p);
   return launched();
 }
 
