@@ -19,11 +19,18 @@ namespace {
 // workgroup each, and a chunk into one run per wave.  A choice's row is
 //   start[g] + (choices of g in earlier chunks) + (in earlier waves of the
 //   chunk) + (earlier in the wave's run),
-// the last from ballots over the bits of g, 64 choices at a time.
+// the last from ballots over the bits of g, 64 choices at a time.  Up to
+// kOneLaunch choices every workgroup counts them all itself (its share of the L2
+// reads costs less than a second launch); beyond, a first kernel leaves each
+// chunk's counts in the workspace.
 constexpr int LT = 512;                  // threads per workgroup
 constexpr int LW = LT / 64;
-constexpr int kChunkLeast = 2048;        // choices per chunk before more workgroups are used
-constexpr int kChunksMost = 64;
+constexpr int LKEEP = 4;                 // choices of its run that a lane keeps in registers
+constexpr int LCOUNT = 8;                // loads in flight while counting
+constexpr int kOneLaunch = LT * LCOUNT;
+constexpr int kShare = 1024;             // choices or rows per workgroup while there are workgroups to add
+constexpr int kWorkgroupsMost = 64;
+constexpr int kCopies = 2048;            // LDS words for copies of the counters
 
 __device__ __forceinline__ int group_of(const LayoutParams& p, int i) {
   const long long g = (long long)p.ids[i] - p.first;
@@ -31,93 +38,137 @@ __device__ __forceinline__ int group_of(const LayoutParams& p, int i) {
   return g >= 0 && g < p.groups - (p.others != 0) ? (int)g : last;
 }
 
-// counts[chunk][g] of each chunk
-__global__ __launch_bounds__(LT) void layout_count_kernel(LayoutParams p, int chunk, int32_t* counts) {
-  extern __shared__ int32_t lds[];
-  for (int g = threadIdx.x; g < p.groups; g += LT) lds[g] = 0;
-  __syncthreads();
-  const int begin = blockIdx.x * chunk, end = min(p.n, begin + chunk);
-  for (int i = begin + (int)threadIdx.x; i < end; i += LT) {
-    const int g = group_of(p, i);
-    if (g >= 0) atomicAdd(&lds[g], 1);
+// add(i, g) for every choice i of [begin, end) that has a group, LCOUNT loads at a time.
+template <typename F>
+__device__ __forceinline__ void count_choices(const LayoutParams& p, int begin, int end, F add) {
+  for (long long i0 = begin + (int)threadIdx.x; i0 < end; i0 += LT * LCOUNT) {
+    int g[LCOUNT];
+#pragma unroll
+    for (int u = 0; u < LCOUNT; ++u) g[u] = group_of(p, (int)min(i0 + u * LT, (long long)end - 1));
+#pragma unroll
+    for (int u = 0; u < LCOUNT; ++u)
+      if (i0 + u * LT < end && g[u] >= 0) add((int)i0 + u * LT, g[u]);
   }
+}
+
+// counts[chunk][g] of each chunk
+__global__ __launch_bounds__(LT) void layout_count_kernel(LayoutParams p, int chunk, int copies, int32_t* counts) {
+  extern __shared__ int32_t lds[];
+  for (int i = threadIdx.x; i < copies * p.groups; i += LT) lds[i] = 0;
   __syncthreads();
-  for (int g = threadIdx.x; g < p.groups; g += LT) counts[(size_t)blockIdx.x * p.groups + g] = lds[g];
+  int32_t* own = lds + (threadIdx.x % copies) * p.groups;
+  const int begin = (int)min((long long)p.n, (long long)blockIdx.x * chunk), end = min(p.n, begin + chunk);
+  count_choices(p, begin, end, [&](int, int g) { atomicAdd(&own[g], 1); });
+  __syncthreads();
+  for (int g = threadIdx.x; g < p.groups; g += LT) {
+    int n = 0;
+    for (int c = 0; c < copies; ++c) n += lds[c * p.groups + g];
+    counts[(size_t)blockIdx.x * p.groups + g] = n;
+  }
 }
 
 // Places one chunk's choices; every workgroup also fills its share of the
 // row-indexed outputs (layout, and slot_of where a row has no choice).
-__global__ __launch_bounds__(LT) void layout_place_kernel(LayoutParams p, int chunk, const int32_t* counts) {
+// The counters of the other chunks are kept in `copies` copies, by lane, so that
+// the lanes of a wave seldom meet when there are few groups.
+__global__ __launch_bounds__(LT) void layout_place_kernel(LayoutParams p, int chunk, int copies,
+                                                          const int32_t* counts) {
   extern __shared__ int32_t lds[];
   const int G = p.groups;
-  int32_t* base = lds;                   // [LW][G]: next row of group g in wave w's run
+  int32_t* base = lds;                   // [LW][G]: next row of group g in wave w's run, from start[g]
   int32_t* total = lds + LW * G;         // [G]: choices of group g
   int32_t* start = total + G;            // [G + 1]: first row of group g
-  int32_t* prev = start + G + 1;         // [G]: choices of group g in earlier chunks
+  int32_t* early = start + G + 1;        // [copies][G]: choices of group g in earlier chunks
+  int32_t* late = early + copies * G;    // [copies][G]: in later chunks
+  __shared__ int wave_span[LW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int begin = min(p.n, (int)blockIdx.x * chunk), end = min(p.n, begin + chunk);
+  const int begin = (int)min((long long)p.n, (long long)blockIdx.x * chunk), end = min(p.n, begin + chunk);
   const int run = (end - begin + LW * 64 - 1) / (LW * 64) * 64;      // choices per wave
   const int wb = min(end, begin + wave * run), we = min(end, wb + run);
-  for (int i = tid; i < (LW + 1) * G; i += LT) lds[i] = 0;
-  for (int g = tid; g < G; g += LT) prev[g] = 0;
+  int kept[LKEEP];                       // groups of this lane's first choices
+#pragma unroll
+  for (int j = 0; j < LKEEP; ++j) kept[j] = wb + 64 * j + lane < we ? group_of(p, wb + 64 * j + lane) : -1;
+  for (int i = tid; i < LW * G; i += LT) base[i] = 0;
+  for (int i = tid; i < 2 * copies * G; i += LT) early[i] = 0;
   __syncthreads();
-  for (int i = wb + lane; i < we; i += 64) {
+#pragma unroll
+  for (int j = 0; j < LKEEP; ++j)
+    if (kept[j] >= 0) atomicAdd(&base[wave * G + kept[j]], 1);
+  for (int i = wb + 64 * LKEEP + lane; i < we; i += 64) {
     const int g = group_of(p, i);
     if (g >= 0) atomicAdd(&base[wave * G + g], 1);
   }
-  if (counts) {                          // more than one chunk: all chunks' counts
-    const int chunks = gridDim.x;
-    for (int i = tid; i < chunks * G; i += LT) {
-      const int g = i % G, v = counts[i];
-      if (v == 0) continue;
-      atomicAdd(&total[g], v);
-      if (i / G < (int)blockIdx.x) atomicAdd(&prev[g], v);
-    }
-  }
-  __syncthreads();
-  if (!counts)
-    for (int g = tid; g < G; g += LT) {
-      int n = 0;
-#pragma unroll
-      for (int w = 0; w < LW; ++w) n += base[w * G + g];
-      total[g] = n;
-    }
-  __syncthreads();
-  // segment starts: an exclusive scan by the first wave (saturating: a row beyond
-  // INT_MAX is beyond p.rows too)
-  if (wave == 0) {
-    long long carry = 0;
-    for (int g0 = 0; g0 < G; g0 += 64) {
-      const int g = g0 + lane;
-      long long span = 0;
-      if (g < G) span = p.align ? ((long long)total[g] + p.align - 1) / p.align * p.align : p.max_m;
-      long long incl = span;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const long long up = __shfl_up(incl, o);
-        if (lane >= o) incl += up;
+  int32_t* mine = early + (tid % copies) * G;
+  if (counts) {                          // one thread per group and part of the chunks
+    const int parts = G < LT ? LT / G : 1;
+    for (int at = tid; at < parts * G; at += LT) {
+      const int g = at % G;
+      int before = 0, after = 0;
+#pragma unroll 8
+      for (int c = at / G; c < (int)gridDim.x; c += parts) {
+        const int v = counts[(size_t)c * G + g];
+        before += c < (int)blockIdx.x ? v : 0;
+        after += c > (int)blockIdx.x ? v : 0;
       }
-      if (g < G) start[g] = (int)min(carry + incl - span, (long long)INT_MAX);
-      carry += __shfl(incl, 63);
+      if (before) atomicAdd(&mine[g], before);
+      if (after) atomicAdd(&mine[copies * G + g], after);
     }
-    if (lane == 0) start[G] = (int)min(carry, (long long)INT_MAX);
+  } else {
+    count_choices(p, 0, p.n, [&](int i, int g) {
+      if (i < begin || i >= end) atomicAdd(&mine[(i < begin ? 0 : copies * G) + g], 1);
+    });
   }
   __syncthreads();
-  for (int g = tid; g < G; g += LT) {    // counts in earlier waves, relative to the segment's start
-    int n = prev[g];
+  // per group: the runs' offsets, the total, and the segments' starts as an
+  // exclusive scan (at most n + G * (align - 1) rows, or masked G * max_m: both fit an int)
+  int carry = 0;
+  for (int g0 = 0; g0 < G; g0 += LT) {
+    const int g = g0 + tid;
+    int span = 0;
+    if (g < G) {
+      int n = 0, rest = 0;
+      for (int c = 0; c < copies; ++c) {
+        n += early[c * G + g];
+        rest += late[c * G + g];
+      }
 #pragma unroll
-    for (int w = 0; w < LW; ++w) {
-      const int c = base[w * G + g];
-      base[w * G + g] = n;
-      n += c;
+      for (int w = 0; w < LW; ++w) {
+        const int c = base[w * G + g];
+        base[w * G + g] = n;
+        n += c;
+      }
+      n += rest;
+      total[g] = n;
+      if (blockIdx.x == 0 && p.counts) p.counts[g] = p.align ? n : min(n, p.max_m);
+      span = p.align ? (n + p.align - 1) / p.align * p.align : p.max_m;
     }
-    if (blockIdx.x == 0 && p.counts) p.counts[g] = p.align ? total[g] : min(total[g], p.max_m);
+    int incl = span;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 63) wave_span[wave] = incl;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < LW; ++w) {
+      if (w < wave) before += wave_span[w];
+      carry += wave_span[w];
+    }
+    if (g < G) start[g] = before + incl - span;
+    __syncthreads();
   }
-  __syncthreads();
   const int bits = 32 - __clz(G);        // ids 0..G-1, and G for a choice without a group
-  for (int i0 = wb; i0 < we; i0 += 64) {
+  for (int j = 0, i0 = wb; i0 < we; ++j, i0 += 64) {
     const int i = i0 + lane;
-    int g = i < we ? group_of(p, i) : -1;
+    int g;
+    switch (j) {                         // kept[j] with a constant index
+      case 0: g = kept[0]; break;
+      case 1: g = kept[1]; break;
+      case 2: g = kept[2]; break;
+      case 3: g = kept[3]; break;
+      default: g = i < we ? group_of(p, i) : -1;
+    }
     const int key = g >= 0 ? g : G;
     uint64_t same = ~0ull;               // lanes with this lane's group
     for (int b = 0; b < bits; ++b) {
@@ -135,9 +186,9 @@ __global__ __launch_bounds__(LT) void layout_place_kernel(LayoutParams p, int ch
     }
     __builtin_amdgcn_wave_barrier();
     if (i < we) {
-      const long long row = g >= 0 ? (long long)start[g] + rank : -1;
+      const int row = g >= 0 ? start[g] + rank : -1;
       const bool fits = g >= 0 && row < p.rows && (p.align || rank < p.max_m);
-      if (p.row_of) p.row_of[i] = fits ? (int)row : -1;
+      if (p.row_of) p.row_of[i] = fits ? row : -1;
       if (fits) p.slot_of[row] = i;
     }
   }
@@ -153,8 +204,8 @@ __global__ __launch_bounds__(LT) void layout_place_kernel(LayoutParams p, int ch
       g = lo;
       rank = (int)(r - start[g]);
     } else {
-      g = (int)(r / p.max_m);
-      rank = (int)(r - (long long)g * p.max_m);
+      g = (int)r / p.max_m;
+      rank = (int)r - g * p.max_m;
     }
     const bool used = rank < total[g];
     if (p.layout) p.layout[r] = used ? g : -1;
@@ -165,17 +216,22 @@ __global__ __launch_bounds__(LT) void layout_place_kernel(LayoutParams p, int ch
 }  // namespace
 
 hipError_t launch_layout(const LayoutParams& p, void* scratch, size_t scratch_bytes, hipStream_t stream) {
-  int chunks = (int)((p.n + (long long)kChunkLeast - 1) / kChunkLeast);
-  chunks = chunks < 1 ? 1 : (chunks > kChunksMost ? kChunksMost : chunks);
-  while (chunks > 1 && (size_t)chunks * p.groups * sizeof(int32_t) > scratch_bytes) --chunks;
-  const int chunk = (int)((p.n + (long long)chunks - 1) / chunks);
-  int32_t* counts = chunks > 1 ? static_cast<int32_t*>(scratch) : nullptr;
-  if (chunks > 1) {
-    layout_count_kernel<<<chunks, LT, sizeof(int32_t) * p.groups, stream>>>(p, chunk, counts);
+  const long long most = p.n > p.rows ? p.n : p.rows;
+  int grid = (int)((most + kShare - 1) / kShare);
+  grid = grid < 1 ? 1 : (grid > kWorkgroupsMost ? kWorkgroupsMost : grid);
+  int copies = kCopies / (2 * p.groups);
+  copies = copies < 1 ? 1 : (copies > 32 ? 32 : copies);
+  int32_t* counts = nullptr;
+  if (p.n > kOneLaunch && (size_t)grid * p.groups * sizeof(int32_t) <= scratch_bytes)
+    counts = static_cast<int32_t*>(scratch);
+  const int chunk = (int)((p.n + (long long)grid - 1) / grid);
+  if (counts) {
+    layout_count_kernel<<<grid, LT, sizeof(int32_t) * copies * p.groups, stream>>>(p, chunk, copies, counts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  layout_place_kernel<<<chunks, LT, sizeof(int32_t) * ((LW + 3) * p.groups + 1), stream>>>(p, chunk, counts);
+  const size_t lds = sizeof(int32_t) * ((LW + 2 + 2 * copies) * (size_t)p.groups + 1);
+  layout_place_kernel<<<grid, LT, lds, stream>>>(p, chunk, copies, counts);
   return hipGetLastError();
 }
 
@@ -226,14 +282,38 @@ struct ScatterParams {
   int pow2;
 };
 
+// The block scales of many rows, row by row: sfa is laid out along the rows, and
+// written from the tokens' side each line would be touched by some 16 workgroups
+// (65536 rows of 7168: 24 us of 142).  The scatter leaves the blocks' maxima in
+// table[T][ld], and here a wave writes 64 neighbouring rows' scales.
+__global__ __launch_bounds__(256) void scatter_scales_kernel(ScatterParams p, const float* table, int ld) {
+  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= (size_t)p.rows) return;
+  const int row = (int)at;
+  const int slot = p.slot_of[row];
+  if (slot < 0 || slot >= (long long)p.T * p.top_k) return;
+  const int KB = p.K / 128;
+  const float w = p.weights ? fabsf(p.weights[slot]) : 1.0f;
+  const float* amax = table + (size_t)(slot / p.top_k) * ld;
+  const int g = row / p.rows_per_group;
+  float* sfa = p.sfa + (size_t)g * KB * p.rows_per_group + (row - g * p.rows_per_group);
+  for (int kb = blockIdx.y * 4; kb < KB; kb += gridDim.y * 4) {
+    const float4 m = *reinterpret_cast<const float4*>(amax + kb);
+    const float v[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (kb + e < KB) sfa[(size_t)(kb + e) * p.rows_per_group] = scale_of(__fmul_rn(w, v[e]), p.pow2);
+  }
+}
+
 constexpr int SJ = 8;                    // rows a thread writes per turn; also lanes per block
 
 // One thread per sixteen values of a token, eight threads per block of 128: the
 // token is read and quantised once and stored to all its rows (without weights;
 // with them the products are quantised per row).  In each group of eight lanes,
 // lane i also works out and stores the scale of row i of the turn.
-template <bool WEIGHTED, bool MASKED>
-__global__ __launch_bounds__(256) void scatter_kernel(ScatterParams p) {
+template <bool WEIGHTED, bool MASKED, bool TABLE>
+__global__ __launch_bounds__(256) void scatter_kernel(ScatterParams p, float* table, int ld) {
   const int per_token = p.K / 16;
   const size_t total = (size_t)p.T * per_token;        // a multiple of 8
   const int lane8 = threadIdx.x & 7;
@@ -252,6 +332,7 @@ __global__ __launch_bounds__(256) void scatter_kernel(ScatterParams p) {
     for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(v[e]));
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+    if (TABLE && lane8 == 0) table[(size_t)t * ld + k / 128] = amax;
     int4 q;
     float sf = 1.0f;
     if constexpr (!WEIGHTED) {
@@ -277,7 +358,7 @@ __global__ __launch_bounds__(256) void scatter_kernel(ScatterParams p) {
         sf = scale_of(__fmul_rn(fabsf(wt[lane8 < left ? lane8 : 0]), amax), p.pow2);
         inv = __fdiv_rn(1.0f, sf);
       }
-      if (mine >= 0 && mine < p.rows) {
+      if (!TABLE && mine >= 0 && mine < p.rows) {
         const int KB = p.K / 128, kb = k / 128;
         if constexpr (MASKED) {
           const int g = mine / p.rows_per_group;
@@ -523,6 +604,7 @@ int launched() {
 
 // ---- argument checks shared by the entry points ------------------------------
 constexpr long long kMaxChoices = 1LL << 30;
+constexpr long long kScaleRows = 32768;
 constexpr long long kMaxGrid = 1 << 23;  // workgroups: a grid's thread count has 32 bits
 
 int check_choices(int T, int top_k) {
@@ -573,10 +655,27 @@ int scatter(const void* x, const float* weights, const int32_t* row_of, const in
   const long long wgs = ((long long)T * (K / 16) + 255) / 256;
   const int grid = (int)(wgs < kMaxGrid ? wgs : kMaxGrid);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (rows_per_group != rows)
-    weights ? scatter_kernel<true, true><<<grid, 256, 0, st>>>(p) : scatter_kernel<false, true><<<grid, 256, 0, st>>>(p);
-  else
-    weights ? scatter_kernel<true, false><<<grid, 256, 0, st>>>(p) : scatter_kernel<false, false><<<grid, 256, 0, st>>>(p);
+  // the scales row by row from kScaleRows rows on, if the workspace has room for the maxima
+  const int ld = (K / 128 + 3) / 4 * 4;
+  float* table = nullptr;
+  if (rows >= kScaleRows) {
+    Scratch sc;
+    s = call_scratch(st, &sc);
+    if (s != DG_OK) return s;
+    if ((size_t)T * ld * sizeof(float) <= sc.bytes) table = reinterpret_cast<float*>(sc.ptr);
+  }
+  if (table) {
+    weights ? scatter_kernel<true, false, true><<<grid, 256, 0, st>>>(p, table, ld)
+            : scatter_kernel<false, false, true><<<grid, 256, 0, st>>>(p, table, ld);
+    const int parts = ld / 4 < 16 ? ld / 4 : 16;
+    scatter_scales_kernel<<<dim3((int)((rows + 255) / 256), parts), 256, 0, st>>>(p, table, ld);
+  } else if (rows_per_group != rows) {
+    weights ? scatter_kernel<true, true, false><<<grid, 256, 0, st>>>(p, nullptr, 0)
+            : scatter_kernel<false, true, false><<<grid, 256, 0, st>>>(p, nullptr, 0);
+  } else {
+    weights ? scatter_kernel<true, false, false><<<grid, 256, 0, st>>>(p, nullptr, 0)
+            : scatter_kernel<false, false, false><<<grid, 256, 0, st>>>(p, nullptr, 0);
+  }
   return launched();
 }
 
