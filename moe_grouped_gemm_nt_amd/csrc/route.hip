@@ -31,17 +31,19 @@ struct RouteParams {
 
 // e^x as 2^(x log2 e) with the product's rounding carried along: relative error
 // below 2e-7 at any x the scores use (the bare product loses |x| units of the
-// last place).
+// last place).  Results below 2^-126 are 0.
 __device__ __forceinline__ float exp_f32(float x) {
   const float log2e = 1.44269502f, log2e_lo = 1.92596303e-8f, ln2 = 0.693147182f;
+  x = fmaxf(x, -150.0f);                 // 0 from here down; also keeps lo finite
   const float hi = x * log2e;
   const float lo = fmaf(x, log2e_lo, fmaf(x, log2e, -hi));
   const float r = __builtin_amdgcn_exp2f(hi);
-  const float c = fmaf(r * ln2, lo, r);
-  return hi < -126.0f ? (hi < -150.0f ? 0.0f : exp2f(hi)) : (hi > 127.9f ? INFINITY : c);
+  return hi < 127.0f ? fmaf(r * ln2, lo, r) : r;
 }
 
-__device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + exp_f32(-x)); }
+// The hardware reciprocal (1 unit of the last place) in place of a division: the
+// scores stay within 3e-7.
+__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
 
 template <bool BF16>
 __device__ __forceinline__ float raw_logit(const void* p, size_t i) {
@@ -247,6 +249,398 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
   }
 }
 
+// ---- the common sizes: sixteen lanes per token -------------------------------
+// A key and its expert in one double: the fp32 key's value with the expert's
+// index in low mantissa bits that the conversion leaves empty, so that doubles
+// compare as (key, lowest index first) and no two are equal.  A comparison and
+// exchange is then one v_max_f64 and one v_min_f64, which run at the rate of
+// their fp32 forms here.
+constexpr int kIndexBits = 11;
+
+__device__ __forceinline__ double pack_key(float key, int e) {
+  const int rest = (1 << kIndexBits) - 1;
+  // a lower index is greater: nearer to zero for negative keys, farther for others
+  const int low = key < 0.0f ? e : rest - e;
+  const double d = (double)fminf(key + 0.0f, FLT_MAX);            // -0 is 0; +inf is finite
+  const uint64_t u = __builtin_bit_cast(uint64_t, d) | (uint64_t)low;
+  return key > -INFINITY ? __builtin_bit_cast(double, u) : -INFINITY;
+}
+__device__ __forceinline__ int key_index(double d) {
+  const int low = (int)(__builtin_bit_cast(uint64_t, d) & ((1 << kIndexBits) - 1));
+  return d < 0.0 ? low : (1 << kIndexBits) - 1 - low;
+}
+
+// max and min without the quieting of NaN that the C functions imply (keys are none)
+__device__ __forceinline__ double max_f64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min_f64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
+// DPP controls that pair the sixteen lanes of a row in four steps
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double row_max(double v) {
+  v = max_f64(v, dpp<kXor1>(v));
+  v = max_f64(v, dpp<kXor2>(v));
+  v = max_f64(v, dpp<kHalfMirror>(v));
+  return max_f64(v, dpp<kMirror>(v));
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp<kXor1>(v));
+  v = fmaxf(v, dpp<kXor2>(v));
+  v = fmaxf(v, dpp<kHalfMirror>(v));
+  return fmaxf(v, dpp<kMirror>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kHalfMirror>(v);
+  return v + dpp<kMirror>(v);
+}
+
+__device__ __forceinline__ void order(double& a, double& b) {     // a >= b afterwards
+  const double hi = max_f64(a, b), lo = min_f64(a, b);
+  a = hi;
+  b = lo;
+}
+
+// Sorts v[LO .. LO + N) falling (N a power of two): Batcher's sort by merging odd
+// and even positions.
+template <int LO, int N, int R>
+__device__ __forceinline__ void merge_falling(double* v) {
+  if constexpr (2 * R < N) {
+    merge_falling<LO, N, 2 * R>(v);
+    merge_falling<LO + R, N, 2 * R>(v);
+#pragma unroll
+    for (int i = LO + R; i + R < LO + N; i += 2 * R) order(v[i], v[i + R]);
+  } else {
+    order(v[LO], v[LO + R]);
+  }
+}
+template <int LO, int N>
+__device__ __forceinline__ void sort_falling(double* v) {
+  if constexpr (N > 1) {
+    sort_falling<LO, N / 2>(v);
+    sort_falling<LO + N / 2, N / 2>(v);
+    merge_falling<LO, N, 1>(v);
+  }
+}
+
+// The D highest of N values, sorted falling, into v[0..D): runs of D are sorted
+// and merged; of two falling runs the D highest are max(a[i], b[D-1-i]), a
+// rising-falling sequence that log2 D rounds put in order.
+template <int N, int D>
+__device__ __forceinline__ void top_falling(double* v) {
+#pragma unroll
+  for (int r = 0; r < N; r += D) sort_falling<0, D>(v + r);
+#pragma unroll
+  for (int r = D; r < N; r += D) {
+#pragma unroll
+    for (int i = 0; i < D; ++i) v[i] = max_f64(v[i], v[r + D - 1 - i]);
+#pragma unroll
+    for (int h = D / 2; h >= 1; h >>= 1)
+#pragma unroll
+      for (int i = 0; i < D; ++i)
+        if ((i & h) == 0) order(v[i], v[i + h]);
+  }
+}
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef u16x4 u16x4_any __attribute__((aligned(2)));
+
+// Sixteen lanes per token: lane l's logits, experts q * 64 + 4 l + i in x[4 q + i]
+// (-inf for masked ones and beyond E).
+template <bool BF16, int NI>
+__device__ __forceinline__ void load16(const void* logits, size_t row, int E, int lane, float (&x)[NI]) {
+#pragma unroll
+  for (int q = 0; q < NI / 4; ++q) {
+    const int e = q * 64 + lane * 4;
+    if (e + 4 <= E) {
+      if constexpr (BF16) {
+        const u16x4 h = *reinterpret_cast<const u16x4_any*>(static_cast<const uint16_t*>(logits) + row + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * q + i] = __uint_as_float((uint32_t)h[i] << 16);
+      } else {
+        const f32x4 h = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(logits) + row + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * q + i] = h[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[4 * q + i] = e + i < E ? raw_logit<BF16>(logits, row + e + i) : -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) x[i] = clean_logit(x[i]);
+}
+
+// y = softmax(x) of the sixteen lanes' values; top and inv, the sum's reciprocal, for single values.
+template <int NI>
+__device__ __forceinline__ void softmax16(const float (&x)[NI], float (&y)[NI], float& top, float& inv) {
+  top = x[0];
+#pragma unroll
+  for (int i = 1; i < NI; ++i) top = fmaxf(top, x[i]);
+  top = row_max(top);
+  float total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    y[i] = x[i] > -INFINITY ? exp_f32(x[i] - top) : 0.0f;
+    total += y[i];
+  }
+  total = row_sum(total);
+  inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) y[i] *= inv;
+}
+
+// Sixteen lanes per token, four tokens per wave: lane l holds experts
+// q * 64 + 4 l .. + 3, so that the sixteen read 256 (or, bf16, 128) contiguous
+// bytes at a time and a lane's four neighbours are of one group (the groups'
+// size is a multiple of 4 here).  Each lane sorts its own keys down to the D
+// highest; a choice is then the highest head of the sixteen lists, four DPP
+// steps, and its owner's list moves up.  Bound by the VALU: about 180
+// instructions per token at 256 experts and 8 choices, where one wave per token
+// that searches all keys for every choice takes some 700.
+template <int NI, int D, bool BF16, bool SIGMOID>
+__global__ __launch_bounds__(256) void route16_kernel(RouteParams p) {
+  constexpr int Q = NI / 4;
+  __shared__ float2 lds_pair[16][16 * Q];      // [token of the workgroup][quad of experts]
+  const int lane = threadIdx.x & 15, local = threadIdx.x >> 4;
+  const size_t t = (size_t)blockIdx.x * 16 + local;
+  const bool live = t < (size_t)p.T;
+  const size_t row = (live ? t : (size_t)p.T - 1) * p.E;
+  float s[NI];
+  load16<BF16>(p.logits, row, p.E, lane, s);
+  float top = 0.0f, inv = 1.0f, keys[NI];
+  double v[NI];
+  if constexpr (SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) keys[i] = sigmoid_f32(s[i]);
+  } else {
+    softmax16(s, keys, top, inv);
+  }
+  if (p.bias) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int e = q * 64 + lane * 4;
+      f32x4 b;
+      if (e + 4 <= p.E)
+        b = *reinterpret_cast<const f32x4_any*>(p.bias + e);
+      else
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = e + i < p.E ? p.bias[e + i] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) keys[4 * q + i] += b[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i)                       // NaN compares false
+    keys[i] = s[i] > -INFINITY && keys[i] > -INFINITY ? keys[i] : -INFINITY;
+  if (p.num_groups > 1) {
+    const int per4 = p.E / p.num_groups / 4;         // quads per group
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float a = fmaxf(keys[4 * q], keys[4 * q + 1]), b = fminf(keys[4 * q], keys[4 * q + 1]);
+      const float c = fmaxf(keys[4 * q + 2], keys[4 * q + 3]), d = fminf(keys[4 * q + 2], keys[4 * q + 3]);
+      b = fmaxf(fminf(a, c), fmaxf(b, d));
+      a = fmaxf(a, c);
+      lds_pair[local][q * 16 + lane] = make_float2(a, b);
+    }
+    // the same wave wrote what these lanes read
+    __builtin_amdgcn_wave_barrier();
+    float a = -INFINITY, b = -INFINITY;
+    if (lane < p.num_groups)
+      for (int j = 0; j < per4; ++j) {
+        const float2 c = lds_pair[local][lane * per4 + j];
+        b = fmaxf(fminf(a, c.x), fmaxf(b, c.y));
+        a = fmaxf(a, c.x);
+      }
+    const double g = pack_key(lane < p.num_groups ? (p.group_top > 1 && b > -INFINITY ? a + b : a) : -INFINITY, lane);
+    // a group's place is the number of groups above it
+    int above = 0;
+    double other = g;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) {
+      other = dpp<0x121>(other);                     // the row turned by one lane
+      above += other > g ? 1 : 0;
+    }
+    const uint64_t ballot = __ballot(above < p.topk_groups && g > -INFINITY);
+    const uint32_t kept = (uint32_t)(ballot >> (threadIdx.x & 48)) & 0xFFFF;
+    const uint32_t magic = 65536 / per4 + 1;         // quad / per4 for quads below 256
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const uint32_t group = ((uint32_t)(q * 16 + lane) * magic) >> 16;
+      const bool in = (kept >> (group & 15)) & 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) keys[4 * q + i] = in ? keys[4 * q + i] : -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) v[i] = pack_key(keys[i], (i >> 2) * 64 + lane * 4 + (i & 3));
+  top_falling<NI, D>(v);
+  double mine = -INFINITY;                           // lane j keeps the j-th choice
+  for (int j = 0; j < p.top_k; ++j) {
+    const double m = row_max(v[0]);
+    if (lane == j) mine = m;
+    const bool owner = v[0] == m;                    // keys differ, except where nothing is left
+#pragma unroll
+    for (int i = 0; i + 1 < D; ++i) {
+      double next = v[i + 1];
+      asm("" : "+v"(next));                          // two selects, and not a load at a selected index
+      v[i] = owner ? next : v[i];
+    }
+    v[D - 1] = owner ? -INFINITY : v[D - 1];
+  }
+  const bool chosen = mine > -INFINITY;
+  const int id = chosen ? key_index(mine) : -1;
+  float w = 0.0f;
+  if (chosen) {
+    const float x = clean_logit(raw_logit<BF16>(p.logits, row + id));
+    w = SIGMOID ? sigmoid_f32(x) : exp_f32(x - top) * inv;
+  }
+  if (p.renormalize) {
+    const float total = row_sum(w);
+    w = total > 0.0f ? w / total : 0.0f;
+  }
+  if (live && lane < p.top_k) {
+    p.ids[t * p.top_k + lane] = id;
+    p.weights[t * p.top_k + lane] = p.scale * w;
+  }
+}
+
+// The gradient, sixteen lanes per token (formulas at route_backward_kernel): lane j
+// on the j-th choice, whose term reaches the expert's lane through LDS.
+template <int NI, bool BF16, bool SIGMOID>
+__global__ __launch_bounds__(256) void route16_backward_kernel(RouteParams p) {
+  __shared__ f32x4 lds_u[16][NI * 4];          // [token of the workgroup][quad of experts]
+  const int lane = threadIdx.x & 15, local = threadIdx.x >> 4;
+  const size_t t = (size_t)blockIdx.x * 16 + local;
+  const bool live = t < (size_t)p.T;
+  const size_t row = (live ? t : (size_t)p.T - 1) * p.E;
+#pragma unroll
+  for (int q = 0; q < NI / 4; ++q) lds_u[local][q * 16 + lane] = f32x4{};
+  int id = -1;
+  float g = 0.0f, xi = -INFINITY;
+  if (live && lane < p.top_k) {
+    id = p.ids[t * p.top_k + lane];
+    if (id < 0 || id >= p.E) id = -1;
+    if (id >= 0) {
+      xi = clean_logit(raw_logit<BF16>(p.logits, row + id));
+      g = p.grad_weights[t * p.top_k + lane] * p.scale;
+    }
+  }
+  // a renormalised sigmoid needs the chosen logits only
+  float y[NI], top = 0.0f, inv = 1.0f;
+  if constexpr (!SIGMOID) {
+    float x[NI];
+    load16<BF16>(p.logits, row, p.E, lane, x);
+    softmax16(x, y, top, inv);
+  }
+  const float s = xi > -INFINITY ? (SIGMOID ? sigmoid_f32(xi) : exp_f32(xi - top) * inv) : 0.0f;
+  float share = s;                             // w_j / scale
+  if (p.renormalize) {
+    const float total = row_sum(s);
+    share = total > 0.0f ? s / total : 0.0f;
+  }
+  float u = s > 0.0f ? g * share : 0.0f;
+  const float sum = row_sum(u);
+  if (p.renormalize) u -= share * sum;
+  // one wave writes and reads a token's words: program order is enough
+  __builtin_amdgcn_wave_barrier();
+  if (id >= 0) reinterpret_cast<float*>(&lds_u[local][0])[id] = SIGMOID ? u * (1.0f - s) : u;
+  __builtin_amdgcn_wave_barrier();
+  if (!live) return;
+  const float back = !SIGMOID && !p.renormalize ? sum : 0.0f;
+#pragma unroll
+  for (int q = 0; q < NI / 4; ++q) {
+    const int e = q * 64 + lane * 4;
+    if (e >= p.E) continue;
+    f32x4 d = lds_u[local][q * 16 + lane];
+    if constexpr (!SIGMOID)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] -= y[4 * q + i] * back;
+    if constexpr (BF16) {
+      u16x4 h;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(d[i]));
+      uint16_t* out = static_cast<uint16_t*>(p.grad_logits) + row + e;
+      if (e + 4 <= p.E)
+        *reinterpret_cast<u16x4_any*>(out) = h;
+      else
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (e + i < p.E) out[i] = h[i];
+    } else {
+      float* out = static_cast<float*>(p.grad_logits) + row + e;
+      if (e + 4 <= p.E)
+        *reinterpret_cast<f32x4_any*>(out) = d;
+      else
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (e + i < p.E) out[i] = d[i];
+    }
+  }
+}
+
+template <int NI>
+void launch_route16_backward(const RouteParams& p, bool bf, int score, hipStream_t st) {
+  const int grid = (int)(((long long)p.T + 15) / 16);
+  if (bf) {
+    if (score == DG_SCORE_SIGMOID)
+      route16_backward_kernel<NI, true, true><<<grid, 256, 0, st>>>(p);
+    else
+      route16_backward_kernel<NI, true, false><<<grid, 256, 0, st>>>(p);
+  } else {
+    if (score == DG_SCORE_SIGMOID)
+      route16_backward_kernel<NI, false, true><<<grid, 256, 0, st>>>(p);
+    else
+      route16_backward_kernel<NI, false, false><<<grid, 256, 0, st>>>(p);
+  }
+}
+
+template <int NI, int D>
+void launch_route16(const RouteParams& p, bool bf, int score, hipStream_t st) {
+  const int grid = (int)(((long long)p.T + 15) / 16);
+  if (bf) {
+    if (score == DG_SCORE_SIGMOID)
+      route16_kernel<NI, D, true, true><<<grid, 256, 0, st>>>(p);
+    else
+      route16_kernel<NI, D, true, false><<<grid, 256, 0, st>>>(p);
+  } else {
+    if (score == DG_SCORE_SIGMOID)
+      route16_kernel<NI, D, false, true><<<grid, 256, 0, st>>>(p);
+    else
+      route16_kernel<NI, D, false, false><<<grid, 256, 0, st>>>(p);
+  }
+}
+
+// Whether sixteen lanes per token do it: up to 512 experts (32 keys a lane), 16
+// choices (one a lane), 16 groups (one a lane) of whole quads.  Other calls take
+// one wave per token.
+bool fits_route16(const RouteParams& p) {
+  return p.E <= 512 && p.top_k <= 16 &&
+         (p.num_groups == 1 || (p.num_groups <= 16 && p.E / p.num_groups % 4 == 0));
+}
+
 template <bool BACK, int NI, bool BF16>
 void launch_score(const RouteParams& p, int score, int grid, hipStream_t st) {
   if constexpr (BACK) {
@@ -264,8 +658,32 @@ void launch_score(const RouteParams& p, int score, int grid, hipStream_t st) {
 
 template <bool BACK>
 int launch_route(const RouteParams& p, int logits_type, int score, hipStream_t st) {
-  const int grid = (int)((p.T + (long long)WAVES - 1) / WAVES);
   const bool bf = logits_type == DG_BF16;
+  if (!BACK && fits_route16(p)) {
+    if (p.E <= 64)
+      launch_route16<4, 4>(p, bf, score, st);
+    else if (p.E <= 128)
+      launch_route16<8, 8>(p, bf, score, st);
+    else if (p.E <= 256)
+      p.top_k <= 8 ? launch_route16<16, 8>(p, bf, score, st) : launch_route16<16, 16>(p, bf, score, st);
+    else
+      p.top_k <= 8 ? launch_route16<32, 8>(p, bf, score, st) : launch_route16<32, 16>(p, bf, score, st);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? DG_OK : fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+  }
+  if (BACK && p.E <= 512 && p.top_k <= 16) {
+    if (p.E <= 64)
+      launch_route16_backward<4>(p, bf, score, st);
+    else if (p.E <= 128)
+      launch_route16_backward<8>(p, bf, score, st);
+    else if (p.E <= 256)
+      launch_route16_backward<16>(p, bf, score, st);
+    else
+      launch_route16_backward<32>(p, bf, score, st);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? DG_OK : fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+  }
+  const int grid = (int)((p.T + (long long)WAVES - 1) / WAVES);
 #define DG_ROUTE_CASE(NI)                                   \
   if (p.E <= 64 * (NI)) {                                   \
     if (bf)                                                 \
