@@ -25,7 +25,7 @@ SOURCES = {
     "dg_api.hip": [],
     "route.hip": [],
     "expert_rows.hip": [],
-    "lora.hip": [],
+    "lora.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 # packed fp32 VALU forms are disabled on purpose: the kernels issue one fp32

@@ -1,10 +1,9 @@
 // Low-rank adapters of many requests beside a shared projection (include/dg.h):
 //   d[t] = c[t] + scales[i] * B[i] . (A[i] . x[t]),   i = adapter_ids[t]
-#include <hip/hip_runtime.h>
-
 #include "../../include/dg.h"
 #include "dg_host.h"
 #include "expert_rows.h"
+#include "fp8_gemm_core.h"    // direct global->LDS loads, waits and the 128-byte row swizzle
 
 namespace dg {
 namespace {
@@ -12,6 +11,7 @@ namespace {
 constexpr int kMaxRank = 256;
 constexpr int THREADS = 256;
 constexpr int WAVES = THREADS / 64;
+constexpr int kStepsMost = 16;
 constexpr int kInlineTokens = 256;       // up to here every workgroup finds its tile's tokens itself
 
 struct LoraParams {
@@ -26,7 +26,10 @@ struct LoraParams {
   int T, N, K, R, L;
   float* partial;          // [k_splits][T][R]: A . x of each K range
   int k_splits;
-  int kb_per_split;        // K blocks of 128 per range
+  int pieces_per_split;    // 64-K pieces per range
+  int tiles;
+  int steps;               // column steps per workgroup of the product with B
+  int parts;               // workgroups per tile of the product with B
   const int32_t* layout;   // tile lists (many tokens): group of each row, L = tokens without an adapter
   const int32_t* slot_of;  // token of each row, -1 where a tile is not full
 };
@@ -35,128 +38,237 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ float bf16_f32(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
-__device__ __forceinline__ uint16_t f32_bf16(float x) {
-  __bf16 h = static_cast<__bf16>(x);
-  return __builtin_bit_cast(uint16_t, h);
-}
+// Two shapes of workgroup.  LISTED (many tokens): a tile of 64 tokens from the
+// layout kernels' lists, 16 to a wave.  Otherwise (few tokens): a tile of 16, the
+// four waves share its K range, or its columns.
+template <bool LISTED>
+constexpr int kTile = LISTED ? 64 : 16;
 
-// The tokens of this workgroup's tile into rows[16 * MT] (-1 where there is none)
+// The tokens of this workgroup's tile into rows[kTile] (-1 where there is none)
 // and their adapter into *id (-1: none).  Returns false for a workgroup without a
 // tile.  Ends with a barrier.
 //
-// INLINE: the workgroup of token t has a tile if the tokens before t hold a
-// multiple of 16 * MT tokens of t's adapter; its tile is t and the next ones of
-// that adapter.  Every wave counts for itself (at most kInlineTokens / 64
-// ballots), so that no workgroup waits for a list.
-template <int MT, bool INLINE>
+// Not LISTED: the workgroup of token t has a tile if the tokens before t hold a
+// multiple of 16 tokens of t's adapter; its tile is t and the next ones of that
+// adapter.  Every wave counts for itself (at most kInlineTokens / 64 ballots), so
+// that no workgroup waits for a list.
+template <bool LISTED>
 __device__ __forceinline__ bool find_tile(const LoraParams& p, int tile, int* rows, int* id) {
-  const int lane = threadIdx.x & 63;
-  if constexpr (INLINE) {
+  constexpr int BT = kTile<LISTED>;
+  if constexpr (LISTED) {
+    const int g = p.layout[(size_t)tile * BT];
+    if (g < 0) return false;
+    *id = g < p.L ? g : -1;
+    if (threadIdx.x < BT) rows[threadIdx.x] = p.slot_of[(size_t)tile * BT + threadIdx.x];
+  } else {
+    const int lane = threadIdx.x & 63;
     auto key = [&](int v) { return v >= 0 && v < p.L ? v : -1; };
     int ids[kInlineTokens / 64];
 #pragma unroll
     for (int i = 0; i < kInlineTokens / 64; ++i)
       ids[i] = i * 64 + lane < p.T ? key(p.ids[i * 64 + lane]) : -2;
     const int mine = key(p.ids[tile]);
-    if (threadIdx.x < 16 * MT) rows[threadIdx.x] = -1;
+    if (threadIdx.x < BT) rows[threadIdx.x] = -1;
     __syncthreads();
     int before = 0, after = 0;
 #pragma unroll
     for (int i = 0; i < kInlineTokens / 64; ++i) {
+      if (i * 64 >= p.T) break;
       const int s = i * 64 + lane;
       before += __popcll(__ballot(ids[i] == mine && s < tile));
       const uint64_t m = __ballot(ids[i] == mine && s >= tile);
       const int at = after + __popcll(m & ((1ull << lane) - 1));
-      if (ids[i] == mine && s >= tile && at < 16 * MT && threadIdx.x < 64) rows[at] = s;
+      if (ids[i] == mine && s >= tile && at < BT && threadIdx.x < 64) rows[at] = s;
       after += __popcll(m);
     }
     *id = mine;
-    if (before % (16 * MT) != 0) return false;
-  } else {
-    const int g = p.layout[(size_t)tile * 16 * MT];
-    if (g < 0) return false;
-    *id = g < p.L ? g : -1;
-    if (threadIdx.x < 16 * MT) rows[threadIdx.x] = p.slot_of[(size_t)tile * 16 * MT + threadIdx.x];
+    if (before % BT != 0) return false;
   }
   __syncthreads();
   return true;
 }
 
-// h = A . x over one K range of one tile of 16 * MT tokens, as h^T: the ranks
-// are the MFMA's rows and the tokens its columns, so that a lane ends with four
-// neighbouring ranks of one token.  The waves take the 32-K quarters of each
-// 128-K block (a row's 256 bytes go to the four waves together) and add up
-// through LDS.  Operands come straight from global memory: each element is used
-// once per tile.
-template <int MT, int RT, bool INLINE>
-__global__ __launch_bounds__(THREADS) void lora_shrink_kernel(LoraParams p) {
-  constexpr int U = MT + RT <= 2 ? 8 : (MT + RT <= 5 ? 4 : 2);     // K blocks in flight
-  __shared__ int rows[16 * MT];
-  __shared__ f32x4 sums[2][MT * RT][64];
-  int id;
-  if (!find_tile<MT, INLINE>(p, blockIdx.x, rows, &id) || id < 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// The item of this workgroup, of `items` = tiles * parts: consecutive workgroups go
+// to the 8 XCDs in turn, and with lists each XCD takes a run of tiles with all
+// their parts, so that an adapter's weights are fetched into one L2.
+template <bool LISTED>
+__device__ __forceinline__ bool find_item(int items, int parts, int* tile, int* part) {
+  int item = blockIdx.x;
+  if (!LISTED && item >= items) return false;
+  if (LISTED) {
+    const int per = (items + 7) / 8;
+    item = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || item >= items) return false;
+  }
+  *tile = item / parts;
+  *part = item - *tile * parts;
+  return true;
+}
+
+// ---- h = A . x ---------------------------------------------------------------
+// One K range of one tile, as h^T: the ranks are the MFMA's rows and the tokens
+// its columns, so that a lane ends with four neighbouring ranks of one token.
+// Bound by x (many tokens) or A (few), each read from memory once.
+//
+// Rows of x and of A come into LDS in pieces of 64 K, one 128-byte line per row,
+// with direct loads of eight whole lines each, and are read from there as MFMA
+// operands.  (Operands loaded straight from memory, 64 bytes of sixteen rows at a
+// time, took about 96 cycles of the CU's memory pipe per load: 97 us against 33
+// for 8192 tokens of 7168 at rank 64.)  A row's 16-byte chunk c lies at
+// c ^ swz(row).
+//
+// A tile begins its range at a piece of its own and wraps round: tokens lie K
+// values apart, and with the tiles in step the rows' same pieces would fall on a
+// few memory channels.
+__device__ __forceinline__ bf16x8 piece_operand(const uint8_t* rows, int row, int chunk) {
+  return *reinterpret_cast<const bf16x8*>(rows + row * 128 + ((chunk ^ swz(row)) << 4));
+}
+
+// Many tokens: 64 to a tile, 16 to a wave; the waves load each piece together
+// into a ring of slots, RING - 1 of them ahead of the products.
+template <int RT>
+__global__ __launch_bounds__(THREADS) void lora_shrink_listed_kernel(LoraParams p) {
+  constexpr int BT = kTile<true>;
+  constexpr int NR = BT + RT * 16;             // rows per piece: tokens, then ranks
+  constexpr int RING = RT <= 4 ? 4 : 3;
+  constexpr int LPW = (NR / 8 + WAVES - 1) / WAVES;          // loads per wave and piece
+  __shared__ int rows[BT];
+  __shared__ __attribute__((aligned(128))) uint8_t ring[RING][NR * 128];
+  int id, tile, split;
+  if (!find_item<true>(p.tiles * p.k_splits, p.k_splits, &tile, &split)) return;
+  if (!find_tile<true>(p, tile, rows, &id) || id < 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g16 = lane >> 4;
-  const int KB = p.K / 128;
-  const int kb0 = blockIdx.y * p.kb_per_split, kb1 = min(KB, kb0 + p.kb_per_split);
-  const int koff = wave * 32 + g16 * 8;
-  const uint16_t* xp[MT];
-  const uint16_t* ap[RT];
+  const int first = split * p.pieces_per_split;
+  const int count = min(p.K / 64 - first, p.pieces_per_split);
+  const int turn = tile % count;
+  const uint16_t* src[LPW];
+  uint32_t dst[LPW];                           // within a slot
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int t = rows[m * 16 + r16];
-    // a column without a token repeats the tile's first: MFMA columns are
-    // independent, and this one is not stored
-    xp[m] = p.x + (size_t)(t >= 0 ? t : rows[0]) * p.ldx + koff;
+  for (int l = 0; l < LPW; ++l) {
+    const int at = min(wave + l * WAVES, NR / 8 - 1);        // the last load again where a wave has none left
+    const int row = at * 8 + (lane >> 3), chunk = (lane & 7) ^ swz(row);
+    dst[l] = at * 1024;
+    if (row < BT)                              // a row without a token repeats the first: its column is not stored
+      src[l] = p.x + (size_t)(rows[row] >= 0 ? rows[row] : rows[0]) * p.ldx + chunk * 8;
+    else                                       // ranks beyond R repeat the last: not stored
+      src[l] = p.a + ((size_t)id * p.R + min(row - BT, p.R - 1)) * p.K + chunk * 8;
+  }
+  const uint32_t ring0 = lds_u32(&ring[0][0]);
+  auto load = [&](int i) {
+    int piece = i + turn;
+    piece = first + (piece < count ? piece : piece - count);
+    const uint32_t slot = ring0 + (uint32_t)(i % RING) * (NR * 128);
+#pragma unroll
+    for (int l = 0; l < LPW; ++l) dma_16(src[l] + (size_t)piece * 64, __builtin_amdgcn_readfirstlane(slot + dst[l]));
+  };
+  f32x4 acc[RT] = {};
+  for (int i = 0; i < RING - 1 && i < count; ++i) load(i);
+  for (int i = 0; i < count; ++i) {
+    // piece i is complete for this wave, then for all; they have also left the
+    // slot of piece i - 1, which the next load fills
+    wait_stages<LPW, RING - 2>(min(RING - 2, count - 1 - i));
+    bare_barrier();
+    if (i + RING - 1 < count) load(i + RING - 1);
+    const uint8_t* slot = ring[i % RING];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bf16x8 xf = piece_operand(slot, wave * 16 + r16, h * 4 + g16);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(piece_operand(slot, BT + r * 16 + r16, h * 4 + g16), xf,
+                                                         acc[r], 0, 0, 0);
+    }
+  }
+  const int token = rows[wave * 16 + r16];
+  if (token < 0) return;
+  float* out = p.partial + ((size_t)split * p.T + token) * p.R;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int at = r * 16 + g16 * 4;
+    if (at < p.R) *reinterpret_cast<f32x4*>(out + at) = acc[r];
+  }
+}
+
+// Few tokens: a tile of 16, whose pieces the four waves take in turn, each with
+// LDS of its own (no barrier), UP pieces at a time and all of them in flight.
+template <int RT>
+__global__ __launch_bounds__(THREADS) void lora_shrink_few_kernel(LoraParams p) {
+  constexpr int UP = RT <= 1 ? 4 : (RT <= 4 ? 2 : 1);
+  constexpr int NR = 16 + RT * 16;
+  __shared__ int rows[16];
+  __shared__ __attribute__((aligned(128))) uint8_t slots[WAVES][UP][NR * 128];
+  int id, tile, split;
+  if (!find_item<false>(p.tiles * p.k_splits, p.k_splits, &tile, &split)) return;
+  if (!find_tile<false>(p, tile, rows, &id) || id < 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g16 = lane >> 4;
+  const int first = split * p.pieces_per_split;
+  const int count = min(p.K / 64 - first, p.pieces_per_split);
+  const int turn = tile % count;
+  const int row8 = lane >> 3;
+  const bool more = rows[8] >= 0;              // more than eight tokens: both halves of x
+  const uint16_t *xs[2], *as[2 * RT];
+#pragma unroll
+  for (int l = 0; l < 2; ++l) {
+    const int row = l * 8 + row8;
+    xs[l] = p.x + (size_t)(rows[row] >= 0 ? rows[row] : rows[0]) * p.ldx + ((lane & 7) ^ swz(row)) * 8;
   }
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-    ap[r] = p.a + ((size_t)id * p.R + min(r * 16 + r16, p.R - 1)) * p.K + koff;   // rows beyond R: not stored
-  f32x4 acc[MT][RT] = {};
-  for (int kb = kb0; kb < kb1; kb += U) {
-    bf16x8 xf[U][MT], af[U][RT];
+  for (int l = 0; l < 2 * RT; ++l) {
+    const int row = l * 8 + row8;
+    as[l] = p.a + ((size_t)id * p.R + min(row, p.R - 1)) * p.K + ((lane & 7) ^ swz(row)) * 8;
+  }
+  const uint32_t base = lds_u32(&slots[wave][0][0]);
+  f32x4 acc[RT] = {};
+  for (int i = wave; i < count; i += WAVES * UP) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const size_t k = (size_t)min(kb + u, kb1 - 1) * 128;
+    for (int u = 0; u < UP; ++u) {
+      if (i + u * WAVES >= count) break;
+      int piece = i + u * WAVES + turn;
+      piece = first + (piece < count ? piece : piece - count);
+      const size_t k = (size_t)piece * 64;
+      const uint32_t slot = base + u * (NR * 128);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) af[u][r] = *reinterpret_cast<const bf16x8*>(ap[r] + k);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) xf[u][m] = *reinterpret_cast<const bf16x8*>(xp[m] + k);
+      for (int l = 0; l < 2 * RT; ++l) dma_16_nt(as[l] + k, __builtin_amdgcn_readfirstlane(slot + 2048 + l * 1024));
+      dma_16(xs[0] + k, __builtin_amdgcn_readfirstlane(slot));
+      if (more) dma_16(xs[1] + k, __builtin_amdgcn_readfirstlane(slot + 1024));
     }
+    wait_vm_lgkm0<0>();
+    asm volatile("" ::: "memory");
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (kb + u >= kb1) break;
+    for (int u = 0; u < UP; ++u) {
+      if (i + u * WAVES >= count) break;
+      const uint8_t* slot = slots[wave][u];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int h = 0; h < 2; ++h) {
+        // without more than eight tokens columns 8..15 repeat 0..7: not stored
+        const bf16x8 xf = piece_operand(slot, more ? r16 : r16 & 7, h * 4 + g16);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-          acc[m][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[u][r], xf[u][m], acc[m][r], 0, 0, 0);
+          acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(piece_operand(slot, 16 + r * 16 + r16, h * 4 + g16), xf,
+                                                           acc[r], 0, 0, 0);
+      }
     }
+    wait_vm_lgkm0<0>();                        // the slots are read before the next round fills them
+    asm volatile("" ::: "memory");
   }
-  if (wave >= 2)
+  // the four waves' sums, in the waves' own LDS
+  f32x4* sums = reinterpret_cast<f32x4*>(slots[wave][0]);
 #pragma unroll
-    for (int i = 0; i < MT * RT; ++i) sums[wave - 2][i][lane] = acc[i / RT][i % RT];
+  for (int r = 0; r < RT; ++r) sums[r * 64 + lane] = acc[r];
   __syncthreads();
-  if (wave < 2)
+  // wave w adds up ranks w, w + 4, ... of the tile's sixteenths
+  const int token = rows[r16];
 #pragma unroll
-    for (int i = 0; i < MT * RT; ++i) acc[i / RT][i % RT] += sums[wave][i][lane];
-  __syncthreads();
-  if (wave == 1)
+  for (int r = 0; r < RT; ++r) {
+    if ((r & (WAVES - 1)) != wave) continue;
+    f32x4 sum = {};
 #pragma unroll
-    for (int i = 0; i < MT * RT; ++i) sums[0][i][lane] = acc[i / RT][i % RT];
-  __syncthreads();
-  if (wave != 0) return;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int t = rows[m * 16 + r16];
-    if (t < 0) continue;
-    float* out = p.partial + ((size_t)blockIdx.y * p.T + t) * p.R;
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int at = r * 16 + g16 * 4;
-      if (at < p.R) *reinterpret_cast<f32x4*>(out + at) = acc[m][r] + sums[0][m * RT + r][lane];
-    }
+    for (int w = 0; w < WAVES; ++w) sum += reinterpret_cast<const f32x4*>(slots[w][0])[r * 64 + lane];
+    const int at = r * 16 + g16 * 4;
+    if (token >= 0 && at < p.R)
+      *reinterpret_cast<f32x4*>(p.partial + ((size_t)split * p.T + token) * p.R + at) = sum;
   }
 }
 
@@ -167,138 +279,311 @@ struct Piece {
   typedef V U __attribute__((aligned(2)));
 };
 
-// d = c + B . h for one tile of tokens and 16 * NT * WAVES columns, again
-// transposed: MFMA rows are columns of d.  h (the K ranges' sum times the
+// ---- d = c + B . h -----------------------------------------------------------
+// Again transposed: MFMA rows are columns of d.  h (the K ranges' sum times the
 // adapter's scale) is split into two bf16, h = hi + lo to 16 bits, and both
 // halves are multiplied: the products with B are then exact to 2^-17.
+template <int BT, int RP>
+__device__ __forceinline__ void sum_h(const LoraParams& p, const int* rows, int id, uint16_t (*hs)[BT][RP + 8]) {
+  const float scale = p.scales ? p.scales[id] : 1.0f;
+  for (int i = threadIdx.x; i < BT * (RP / 4); i += THREADS) {
+    const int at = i / (RP / 4), r = i % (RP / 4) * 4;
+    const int t = rows[at];
+    f32x4 h = {};
+    if (t >= 0 && r < p.R)
+#pragma unroll 4
+      for (int s = 0; s < p.k_splits; ++s)
+        h += *reinterpret_cast<const f32x4*>(p.partial + ((size_t)s * p.T + t) * p.R + r);
+    u16x4 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v = h[e] * scale;
+      hi[e] = f32_to_bf16(v);
+      const float back = bf16_to_f32(hi[e]);
+      lo[e] = fabsf(back) < INFINITY ? f32_to_bf16(v - back) : 0;
+    }
+    *reinterpret_cast<u16x4*>(&hs[0][at][r]) = hi;
+    *reinterpret_cast<u16x4*>(&hs[1][at][r]) = lo;
+  }
+}
+
+// Few tokens: a tile of 16, the waves side by side on 16 * NT columns each.
 // MFMA row r of sub-tile j stands for column 4 * NT * (r / 4) + 4 * j + r % 4, so
 // that a lane's 4 * NT results are neighbours in d.
-template <int MT, int RK, int NT, bool INLINE>
-__global__ __launch_bounds__(THREADS) void lora_expand_kernel(LoraParams p) {
+template <int RK, int NT>
+__global__ __launch_bounds__(THREADS) void lora_expand_few_kernel(LoraParams p) {
   constexpr int RP = RK * 32;             // ranks padded to whole MFMA steps
   constexpr int LD = RP + 8;              // LDS row: 16 bytes on, so that 16 rows start in different banks
   constexpr int NE = 4 * NT;
-  __shared__ int rows[16 * MT];
-  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16 * MT][LD];
-  int id;
-  if (!find_tile<MT, INLINE>(p, blockIdx.x, rows, &id)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  typedef typename Piece<NE>::U U;
+  __shared__ int rows[16];
+  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][LD];
+  int id, tile, part;
+  if (!find_item<false>(p.tiles * p.parts, p.parts, &tile, &part)) return;
+  if (!find_tile<false>(p, tile, rows, &id)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g16 = lane >> 4;
-  const int col0 = (blockIdx.y * WAVES + wave) * 16 * NT;      // this wave's first column
-  f32x4 acc[MT][NT] = {};
+  const int col = (part * WAVES + wave) * 16 * NT;             // this wave's first column
+  const int token = rows[r16];
+  const int n = col + NE * g16;
+  U v = {};                               // a column without a token reads the tile's first
+  if (p.c && n + NE <= p.N) v = *reinterpret_cast<const U*>(p.c + (size_t)(token >= 0 ? token : rows[0]) * p.ldc + n);
+  f32x4 acc[NT] = {};
   if (id >= 0) {
-    const float scale = p.scales ? p.scales[id] : 1.0f;
     bf16x8 bf[NT][RK];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int n = min(col0 + 4 * NT * (r16 >> 2) + 4 * j + (r16 & 3), p.N - 1);    // beyond N: not stored
-      const uint16_t* b = p.b + ((size_t)id * p.N + n) * p.R + g16 * 8;
+      const int at = min(col + NE * (r16 >> 2) + 4 * j + (r16 & 3), p.N - 1);         // beyond N: not stored
+      const uint16_t* b = p.b + ((size_t)id * p.N + at) * p.R + g16 * 8;
 #pragma unroll
       for (int k = 0; k < RK; ++k) {
         bf[j][k] = bf16x8{};
         if (k * 32 + g16 * 8 < p.R) bf[j][k] = *reinterpret_cast<const bf16x8*>(b + k * 32);
       }
     }
-    for (int i = threadIdx.x; i < 16 * MT * (RP / 4); i += THREADS) {
-      const int row = i / (RP / 4), r = i % (RP / 4) * 4;
-      const int t = rows[row];
-      f32x4 h = {};
-      if (t >= 0 && r < p.R)
-        for (int s = 0; s < p.k_splits; ++s)
-          h += *reinterpret_cast<const f32x4*>(p.partial + ((size_t)s * p.T + t) * p.R + r);
-      u16x4 hi, lo;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = h[e] * scale;
-        hi[e] = f32_bf16(v);
-        const float back = bf16_f32(hi[e]);
-        lo[e] = fabsf(back) < INFINITY ? f32_bf16(v - back) : 0;
-      }
-      *reinterpret_cast<u16x4*>(&hs[0][row][r]) = hi;
-      *reinterpret_cast<u16x4*>(&hs[1][row][r]) = lo;
-    }
+    sum_h<16, RP>(p, rows, id, hs);
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int k = 0; k < RK; ++k)
 #pragma unroll
-      for (int k = 0; k < RK; ++k)
+      for (int q = 0; q < 2; ++q) {
+        const bf16x8 h = *reinterpret_cast<const bf16x8*>(&hs[q][r16][k * 32 + g16 * 8]);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const bf16x8 h = *reinterpret_cast<const bf16x8*>(&hs[q][m * 16 + r16][k * 32 + g16 * 8]);
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][k], h, acc[m][j], 0, 0, 0);
-        }
+        for (int j = 0; j < NT; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][k], h, acc[j], 0, 0, 0);
+      }
   }
-  typedef typename Piece<NE>::U U;
-  const int n = col0 + NE * g16;
+  if (token < 0 || n >= p.N) return;
+  uint16_t* d = p.d + (size_t)token * p.ldd + n;
+  if (n + NE <= p.N) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int t = rows[m * 16 + r16];
-    if (t < 0 || n >= p.N) continue;
-    const uint16_t* c = p.c ? p.c + (size_t)t * p.ldc + n : nullptr;
-    uint16_t* d = p.d + (size_t)t * p.ldd + n;
-    if (n + NE <= p.N) {
-      U v = {};
-      if (c) v = *reinterpret_cast<const U*>(c);
+    for (int e = 0; e < NE; ++e)
+      if (id >= 0) v[e] = f32_to_bf16(bf16_to_f32(v[e]) + acc[e >> 2][e & 3]);
+    *reinterpret_cast<U*>(d) = v;
+  } else {
+    const uint16_t* c = p.c ? p.c + (size_t)token * p.ldc + n : nullptr;
 #pragma unroll
-      for (int e = 0; e < NE; ++e)
-        if (id >= 0) v[e] = f32_bf16(bf16_f32(v[e]) + acc[m][e >> 2][e & 3]);
-      *reinterpret_cast<U*>(d) = v;
-    } else {
+    for (int e = 0; e < NE; ++e)
+      if (n + e < p.N) {
+        const uint16_t w = c ? c[e] : 0;
+        d[e] = id >= 0 ? f32_to_bf16(bf16_to_f32(w) + acc[e >> 2][e & 3]) : w;
+      }
+  }
+}
+
+// Many tokens: 64 to a tile, 16 to a wave, `steps` times 64 columns.  B's 64 rows
+// of a step are contiguous and come into LDS for the four waves with direct
+// loads, a step ahead; results pass through LDS so that c and d are read and
+// written in whole 128-byte lines (8 rows of 64 columns per instruction).  Bound
+// by c and d.
+template <int RK>
+__global__ __launch_bounds__(THREADS) void lora_expand_listed_kernel(LoraParams p) {
+  constexpr int BT = kTile<true>;
+  constexpr int RP = RK * 32;
+  constexpr int OLD = 68;                 // a row of results in LDS: 64 and 16 bytes on
+  typedef typename Piece<8>::U U;
+  union Shared {
+    uint16_t hs[2][BT][RP + 8];
+    float out[WAVES][16][OLD];
+  };
+  __shared__ int rows[BT];
+  __shared__ __attribute__((aligned(16))) Shared sh;
+  __shared__ __attribute__((aligned(128))) uint8_t ring[2][64 * RP * 2];
+  int id, tile, part;
+  if (!find_item<true>(p.tiles * p.parts, p.parts, &tile, &part)) return;
+  if (!find_tile<true>(p, tile, rows, &id)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g16 = lane >> 4, row8 = lane >> 3, col8 = (lane & 7) * 8;
+  const int first = part * p.steps;
+  const int count = min(p.steps, (p.N + 63) / 64 - first);
+  int token[2];                           // rows row8 and row8 + 8 of the wave's sixteen
+  token[0] = rows[wave * 16 + row8];
+  token[1] = rows[wave * 16 + 8 + row8];
+  const bool both = rows[wave * 16 + 8] >= 0;                  // each half of the sixteen has a token: two stores a step
+  const int some = rows[0];
+  U cv[2] = {};
+  auto load_c = [&](int step) {
+    const int n = (first + step) * 64 + col8;
+    if (p.c && n + 8 <= p.N)
 #pragma unroll
-      for (int e = 0; e < NE; ++e)
-        if (n + e < p.N) {
-          const uint16_t v = c ? c[e] : 0;
-          d[e] = id >= 0 ? f32_bf16(bf16_f32(v) + acc[m][e >> 2][e & 3]) : v;
-        }
+      for (int h = 0; h < 2; ++h)         // a row without a token reads the tile's first
+        cv[h] = *reinterpret_cast<const U*>(p.c + (size_t)(token[h] >= 0 ? token[h] : some) * p.ldc + n);
+  };
+  auto store = [&](int step, auto value) {                     // value(h, e): what is added to column e of half h
+    const int n = (first + step) * 64 + col8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (token[h] < 0 || n >= p.N) continue;
+      uint16_t* d = p.d + (size_t)token[h] * p.ldd + n;
+      if (n + 8 <= p.N) {
+        U v = cv[h];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = value(h, e, v[e]);
+        *reinterpret_cast<U*>(d) = v;
+      } else {
+        const uint16_t* c = p.c ? p.c + (size_t)token[h] * p.ldc + n : nullptr;
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+          if (n + e < p.N) d[e] = value(h, e, c ? c[e] : (uint16_t)0);
+      }
     }
+  };
+  if (id < 0) {                           // no adapter: c as it is
+    for (int step = 0; step < count; ++step) {
+      load_c(step);
+      store(step, [](int, int, uint16_t c) { return c; });
+    }
+    return;
+  }
+  // B: chunk q (16 bytes) of the step's 64 rows lies at q, its row's chunks turned by
+  // the row where their number is a power of two
+  const int row_chunks = p.R / 8;
+  const int turn = (row_chunks & (row_chunks - 1)) == 0 ? row_chunks - 1 : 0;
+  int bcol[RK], bchunk[RK];
+  uint32_t bdst[RK];
+#pragma unroll
+  for (int l = 0; l < RK; ++l) {
+    const int at = min(wave + l * WAVES, row_chunks - 1);      // the last load again where a wave has none left
+    const int q = at * 64 + lane;
+    bcol[l] = q / row_chunks;
+    bchunk[l] = (q - bcol[l] * row_chunks) ^ (bcol[l] & turn);
+    bdst[l] = at * 1024;
+  }
+  const uint32_t ring0 = lds_u32(&ring[0][0]);
+  auto load_b = [&](int step) {
+    const uint32_t slot = ring0 + (uint32_t)(step & 1) * (64 * RP * 2);
+#pragma unroll
+    for (int l = 0; l < RK; ++l) {
+      const int n = min((first + step) * 64 + bcol[l], p.N - 1);             // beyond N: not stored
+      dma_16(p.b + ((size_t)id * p.N + n) * p.R + bchunk[l] * 8, __builtin_amdgcn_readfirstlane(slot + bdst[l]));
+    }
+  };
+  load_b(0);
+  load_c(0);
+  sum_h<BT, RP>(p, rows, id, sh.hs);
+  __syncthreads();
+  bf16x8 hf[RK][2];
+#pragma unroll
+  for (int k = 0; k < RK; ++k)
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      hf[k][q] = *reinterpret_cast<const bf16x8*>(&sh.hs[q][wave * 16 + r16][k * 32 + g16 * 8]);
+  for (int step = 0; step < count; ++step) {
+    // this step's B is complete: only the last step's stores, issued after it, may
+    // be under way; and every wave has left the other slot and, at first, hs
+    if (step > 0 && both)
+      wait_vm_lgkm0<2>();
+    else
+      wait_vm_lgkm0<0>();
+    bare_barrier();
+    const U now[2] = {cv[0], cv[1]};
+    if (step + 1 < count) {
+      load_b(step + 1);
+      load_c(step + 1);
+    }
+    const U next[2] = {cv[0], cv[1]};
+    const uint8_t* slot = ring[step & 1];
+    f32x4 acc[4] = {};
+#pragma unroll
+    for (int k = 0; k < RK; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = j * 16 + r16, chunk = k * 4 + g16;
+        bf16x8 bf = {};
+        if (chunk < row_chunks)
+          bf = *reinterpret_cast<const bf16x8*>(slot + (row * row_chunks + (chunk ^ (row & turn))) * 16);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf, hf[k][0], acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf, hf[k][1], acc[j], 0, 0, 0);
+      }
+    // a wave's own rows: program order is enough
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4*>(&sh.out[wave][r16][j * 16 + g16 * 4]) = acc[j];
+    __builtin_amdgcn_wave_barrier();
+    f32x4 sum[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        sum[h][e] = *reinterpret_cast<const f32x4*>(&sh.out[wave][h * 8 + row8][col8 + e * 4]);
+    __builtin_amdgcn_wave_barrier();
+    cv[0] = now[0];
+    cv[1] = now[1];
+    store(step, [&](int h, int e, uint16_t c) { return f32_to_bf16(bf16_to_f32(c) + sum[h][e >> 2][e & 3]); });
+    cv[0] = next[0];
+    cv[1] = next[1];
   }
 }
 
-template <int MT, bool INLINE>
-void launch_shrink(const LoraParams& p, int tiles, hipStream_t st) {
-  const dim3 grid(tiles, p.k_splits);
+template <bool LISTED, int RT>
+void launch_shrink_rt(const LoraParams& p, int grid, hipStream_t st) {
+  if constexpr (LISTED)
+    lora_shrink_listed_kernel<RT><<<grid, THREADS, 0, st>>>(p);
+  else
+    lora_shrink_few_kernel<RT><<<grid, THREADS, 0, st>>>(p);
+}
+
+template <bool LISTED>
+void launch_shrink(const LoraParams& p, hipStream_t st) {
+  const int grid = (p.tiles * p.k_splits + 7) / 8 * 8;
   if (p.R <= 16)
-    lora_shrink_kernel<MT, 1, INLINE><<<grid, THREADS, 0, st>>>(p);
+    launch_shrink_rt<LISTED, 1>(p, grid, st);
   else if (p.R <= 32)
-    lora_shrink_kernel<MT, 2, INLINE><<<grid, THREADS, 0, st>>>(p);
+    launch_shrink_rt<LISTED, 2>(p, grid, st);
   else if (p.R <= 64)
-    lora_shrink_kernel<MT, 4, INLINE><<<grid, THREADS, 0, st>>>(p);
+    launch_shrink_rt<LISTED, 4>(p, grid, st);
   else if (p.R <= 128)
-    lora_shrink_kernel<MT, 8, INLINE><<<grid, THREADS, 0, st>>>(p);
-  else if constexpr (MT == 1)
-    lora_shrink_kernel<MT, 16, INLINE><<<grid, THREADS, 0, st>>>(p);
+    launch_shrink_rt<LISTED, 8>(p, grid, st);
+  else
+    launch_shrink_rt<LISTED, 16>(p, grid, st);
 }
 
-template <int MT, int NT, bool INLINE>
-void launch_expand(const LoraParams& p, int tiles, hipStream_t st) {
-  const dim3 grid(tiles, (p.N + 16 * NT * WAVES - 1) / (16 * NT * WAVES));
+template <int NT>
+void launch_expand_few(LoraParams p, hipStream_t st) {
+  p.parts = (p.N + 16 * NT * WAVES - 1) / (16 * NT * WAVES);
+  const int grid = p.tiles * p.parts;
   if (p.R <= 32)
-    lora_expand_kernel<MT, 1, NT, INLINE><<<grid, THREADS, 0, st>>>(p);
+    lora_expand_few_kernel<1, NT><<<grid, THREADS, 0, st>>>(p);
   else if (p.R <= 64)
-    lora_expand_kernel<MT, 2, NT, INLINE><<<grid, THREADS, 0, st>>>(p);
+    lora_expand_few_kernel<2, NT><<<grid, THREADS, 0, st>>>(p);
   else if (p.R <= 128)
-    lora_expand_kernel<MT, 4, NT, INLINE><<<grid, THREADS, 0, st>>>(p);
-  else if constexpr (MT == 1)
-    lora_expand_kernel<MT, 8, NT, INLINE><<<grid, THREADS, 0, st>>>(p);
+    lora_expand_few_kernel<4, NT><<<grid, THREADS, 0, st>>>(p);
+  else
+    lora_expand_few_kernel<8, NT><<<grid, THREADS, 0, st>>>(p);
 }
 
-// K ranges: enough workgroups to fill the chip twice, at least one block each.
-int k_splits_for(long long tiles, int KB, int num_cus) {
-  const long long want = (2LL * num_cus + tiles - 1) / tiles;
-  return (int)(want < 1 ? 1 : (want > KB ? KB : want));
+void launch_expand_listed(LoraParams p, int num_cus, hipStream_t st) {
+  const int chunks = (p.N + 63) / 64;
+  // several steps per workgroup share one sum of h, as long as two workgroups per CU remain
+  const long long steps = (long long)p.tiles * chunks / (2 * num_cus);
+  p.steps = steps < 1 ? 1 : (steps > kStepsMost ? kStepsMost : (int)steps);
+  p.parts = (chunks + p.steps - 1) / p.steps;
+  const int grid = (p.tiles * p.parts + 7) / 8 * 8;
+  if (p.R <= 32)
+    lora_expand_listed_kernel<1><<<grid, THREADS, 0, st>>>(p);
+  else if (p.R <= 64)
+    lora_expand_listed_kernel<2><<<grid, THREADS, 0, st>>>(p);
+  else if (p.R <= 128)
+    lora_expand_listed_kernel<4><<<grid, THREADS, 0, st>>>(p);
+  else
+    lora_expand_listed_kernel<8><<<grid, THREADS, 0, st>>>(p);
+}
+
+// K ranges: two workgroups per CU at the most, which all run at once (a third
+// round for a few of them would cost as much as the others together), and at
+// least a piece for each of the four waves.
+int k_splits_for(long long tiles, int pieces, int num_cus) {
+  const long long fit = 2LL * num_cus / tiles;
+  const long long most = pieces / WAVES;
+  const long long n = fit < most ? fit : most;
+  return (int)(n < 1 ? 1 : n);
 }
 
 constexpr int kNoRoom = 1;               // not a dg_status: the scratch memory is too small for so many tokens
 
 int lora_tokens(LoraParams p, const Scratch& sc, hipStream_t st) {
-  const int KB = p.K / 128;
+  const int pieces = p.K / 64;
   const bool terms = p.L > 0;
   const bool listed = p.T > kInlineTokens;
-  // tokens per tile: 16 where every workgroup finds its own tokens and for the
-  // largest ranks (their accumulators fill the registers), 64 otherwise
-  const int bt = listed && p.R <= 128 ? 64 : 16;
+  const int bt = listed ? kTile<true> : kTile<false>;
   const int groups = p.L + 1;
   long long rows = p.T;
   size_t list_bytes = 0;
@@ -308,16 +593,17 @@ int lora_tokens(LoraParams p, const Scratch& sc, hipStream_t st) {
     list_bytes = (size_t)(2 * rows + 64) / 64 * 64 * sizeof(int32_t);
   }
   const long long tiles = listed ? rows / bt : p.T;
+  p.tiles = (int)tiles;
   p.k_splits = 1;
-  p.kb_per_split = KB;
+  p.pieces_per_split = pieces;
   if (terms) {
     const size_t one = (size_t)p.T * p.R * sizeof(float);
     if (list_bytes + one > sc.bytes) return kNoRoom;
-    int splits = k_splits_for(listed ? tiles : (p.T < p.L ? p.T : p.L), KB, sc.num_cus);
+    int splits = k_splits_for(listed ? tiles : (p.T < p.L ? p.T : p.L), pieces, sc.num_cus);
     const size_t room = (sc.bytes - list_bytes) / one;
     if ((size_t)splits > room) splits = (int)room;
-    p.kb_per_split = (KB + splits - 1) / splits;
-    p.k_splits = (KB + p.kb_per_split - 1) / p.kb_per_split;
+    p.pieces_per_split = (pieces + splits - 1) / splits;
+    p.k_splits = (pieces + p.pieces_per_split - 1) / p.pieces_per_split;
     p.partial = reinterpret_cast<float*>(sc.ptr + list_bytes);
   } else if (list_bytes > sc.bytes) {
     return kNoRoom;
@@ -332,17 +618,16 @@ int lora_tokens(LoraParams p, const Scratch& sc, hipStream_t st) {
     const hipError_t e = launch_layout(lp, sc.ptr + list_bytes, sc.bytes - list_bytes, st);
     if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
   }
-  // 64 columns per wave, or 16 where that would leave most of the chip without work
-  const bool wide = tiles * ((p.N + 255) / 256) >= 2 * sc.num_cus;
-  if (!listed) {
-    if (terms) launch_shrink<1, true>(p, (int)tiles, st);
-    if (wide) launch_expand<1, 4, true>(p, (int)tiles, st); else launch_expand<1, 1, true>(p, (int)tiles, st);
-  } else if (bt == 64) {
-    if (terms) launch_shrink<4, false>(p, (int)tiles, st);
-    if (wide) launch_expand<4, 4, false>(p, (int)tiles, st); else launch_expand<4, 1, false>(p, (int)tiles, st);
+  if (listed) {
+    if (terms) launch_shrink<true>(p, st);
+    launch_expand_listed(p, sc.num_cus, st);
   } else {
-    if (terms) launch_shrink<1, false>(p, (int)tiles, st);
-    if (wide) launch_expand<1, 4, false>(p, (int)tiles, st); else launch_expand<1, 1, false>(p, (int)tiles, st);
+    if (terms) launch_shrink<false>(p, st);
+    // 64 columns per wave, or 16 where that would leave most of the chip without work
+    if (tiles * ((p.N + 255) / 256) >= 2 * sc.num_cus)
+      launch_expand_few<4>(p, st);
+    else
+      launch_expand_few<1>(p, st);
   }
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? DG_OK : fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
