@@ -27,7 +27,7 @@ constexpr int LT = 512;                  // threads per workgroup
 constexpr int LW = LT / 64;
 constexpr int LKEEP = 4;                 // choices of its run that a lane keeps in registers
 constexpr int LCOUNT = 8;                // loads in flight while counting
-constexpr int kOneLaunch = LT * LCOUNT;
+constexpr int kOneLaunch = 8192;
 constexpr int kShare = 1024;             // choices or rows per workgroup while there are workgroups to add
 constexpr int kWorkgroupsMost = 64;
 constexpr int kCopies = 2048;            // LDS words for copies of the counters
@@ -258,14 +258,13 @@ __device__ __forceinline__ float scale_of(float amax, bool pow2) {
   return sf;
 }
 
-// Four e4m3 codes of clamp(v * inv) packed in an int; NaN stays NaN.
-__device__ __forceinline__ float clamp_e4m3(float v) {
-  const float c = fminf(fmaxf(v, -kE4m3Max), kE4m3Max);
-  return v == v ? c : v;
-}
+// Four e4m3 codes packed in an int, rounded to nearest even.  Products of a value
+// and its block's 1 / sf need no clamp: sf and 1 / sf round to 2^-24 each, so they
+// exceed 448 by less than 2^-22 of it, which rounds to 448 (the next step would
+// begin at 464).  NaN, also from an infinity times 0, gives the NaN code.
 __device__ __forceinline__ int pack_e4m3(float a, float b, float c, float d) {
-  int r = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(a), clamp_e4m3(b), 0, false);
-  return __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(c), clamp_e4m3(d), r, true);
+  const int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
 }
 
 struct ScatterParams {
@@ -396,52 +395,62 @@ struct KScatterParams {
 };
 
 // One workgroup per 128 rows x 128 columns: 16 threads across (8 columns each),
-// 16 rows in flight, 8 rows per thread.
+// 16 rows in flight, 8 rows per thread.  The rows stay in registers between the
+// columns' maxima and the codes; one thread per column works out its scale.
+// Bound by the bytes: a row is read and written once.
 __global__ __launch_bounds__(256) void kscatter_kernel(KScatterParams p) {
-  __shared__ float lds[16][128];
+  __shared__ float part[16][128];
+  __shared__ float inverse[128];
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int row0 = blockIdx.y * 128;
+  const size_t row0 = (size_t)blockIdx.y * 128;
   const int col = blockIdx.x * 128 + tx * 8;
   const bool in = col < p.N;               // N % 16 == 0: whole 8-column pieces
-  float v[8][8], amax[8] = {};
+  int slot[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) slot[i] = p.slot_of[row0 + ty + 16 * i];
+  u16x8 h[8];
+  float w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int slot = p.slot_of[row0 + ty + 16 * i];
-    const bool live = in && slot >= 0 && slot < (long long)p.T * p.top_k;
-    u16x8 h = {};
-    float w = 1.0f;
+    const bool live = in && slot[i] >= 0 && slot[i] < (long long)p.T * p.top_k;
+    h[i] = u16x8{};
+    w[i] = 0.0f;                           // a row without a choice: zeros
     if (live) {
-      h = *reinterpret_cast<const u16x8*>(p.x + (size_t)(slot / p.top_k) * p.N + col);
-      if (p.weights) w = p.weights[slot];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[i][j] = live ? __fmul_rn(w, bf16_f32(h[j])) : 0.0f;
-      amax[j] = fmaxf(amax[j], fabsf(v[i][j]));
+      h[i] = *reinterpret_cast<const u16x8*>(p.x + (size_t)(slot[i] / p.top_k) * p.N + col);
+      w[i] = p.weights ? p.weights[slot[i]] : 1.0f;
     }
   }
+  float amax[8] = {};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) lds[ty][tx * 8 + j] = amax[j];
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax[j] = fmaxf(amax[j], fabsf(__fmul_rn(w[i], bf16_f32(h[i][j]))));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[ty][tx * 8 + j] = amax[j];
   __syncthreads();
-  float inv[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  if (threadIdx.x < 128) {
     float m = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) m = fmaxf(m, lds[r][tx * 8 + j]);
+    for (int r = 0; r < 16; ++r) m = fmaxf(m, part[r][threadIdx.x]);
     const float sf = scale_of(m, p.pow2);
-    inv[j] = __fdiv_rn(1.0f, sf);
-    if (in && ty == 0) p.sfa[(size_t)blockIdx.y * p.N + col + j] = sf;
+    inverse[threadIdx.x] = __fdiv_rn(1.0f, sf);
+    const int c = blockIdx.x * 128 + threadIdx.x;
+    if (c < p.N) p.sfa[(size_t)blockIdx.y * p.N + c] = sf;
   }
+  __syncthreads();
   if (!in) return;
+  float inv[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) inv[j] = inverse[tx * 8 + j];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], inv[j]);
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(w[i], bf16_f32(h[i][j])), inv[j]);
     int2 q;
-    q.x = pack_e4m3(v[i][0], v[i][1], v[i][2], v[i][3]);
-    q.y = pack_e4m3(v[i][4], v[i][5], v[i][6], v[i][7]);
-    *reinterpret_cast<int2*>(p.a + (size_t)(row0 + ty + 16 * i) * p.N + col) = q;
+    q.x = pack_e4m3(v[0], v[1], v[2], v[3]);
+    q.y = pack_e4m3(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<int2*>(p.a + (row0 + ty + 16 * i) * p.N + col) = q;
   }
 }
 

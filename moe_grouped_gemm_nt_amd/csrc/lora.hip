@@ -130,7 +130,7 @@ template <int RT>
 __global__ __launch_bounds__(THREADS) void lora_shrink_listed_kernel(LoraParams p) {
   constexpr int BT = kTile<true>;
   constexpr int NR = BT + RT * 16;             // rows per piece: tokens, then ranks
-  constexpr int RING = RT <= 4 ? 4 : 3;
+  constexpr int RING = 3;
   constexpr int LPW = (NR / 8 + WAVES - 1) / WAVES;          // loads per wave and piece
   __shared__ int rows[BT];
   __shared__ __attribute__((aligned(128))) uint8_t ring[RING][NR * 128];
@@ -567,11 +567,11 @@ void launch_expand_listed(LoraParams p, int num_cus, hipStream_t st) {
     lora_expand_listed_kernel<8><<<grid, THREADS, 0, st>>>(p);
 }
 
-// K ranges: two workgroups per CU at the most, which all run at once (a third
-// round for a few of them would cost as much as the others together), and at
-// least a piece for each of the four waves.
-int k_splits_for(long long tiles, int pieces, int num_cus) {
-  const long long fit = 2LL * num_cus / tiles;
+// K ranges: as many workgroups as run at once (three per CU with lists, by their
+// LDS; a further round for a few of them would cost as much as the others
+// together), and at least a piece for each of the four waves.
+int k_splits_for(bool listed, long long tiles, int pieces, int num_cus) {
+  const long long fit = (listed ? 3LL : 2LL) * num_cus / tiles;
   const long long most = pieces / WAVES;
   const long long n = fit < most ? fit : most;
   return (int)(n < 1 ? 1 : n);
@@ -599,7 +599,7 @@ int lora_tokens(LoraParams p, const Scratch& sc, hipStream_t st) {
   if (terms) {
     const size_t one = (size_t)p.T * p.R * sizeof(float);
     if (list_bytes + one > sc.bytes) return kNoRoom;
-    int splits = k_splits_for(listed ? tiles : (p.T < p.L ? p.T : p.L), pieces, sc.num_cus);
+    int splits = k_splits_for(listed, listed ? tiles : (p.T < p.L ? p.T : p.L), pieces, sc.num_cus);
     const size_t room = (sc.bytes - list_bytes) / one;
     if ((size_t)splits > room) splits = (int)room;
     p.pieces_per_split = (pieces + splits - 1) / splits;
