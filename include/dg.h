@@ -334,7 +334,8 @@ int dg_m_grouped_layout_masked(const int32_t* topk_ids, int T, int top_k, int fi
  * per row per 128 values: for every choice i = t * top_k + j with row r = row_of[i],
  *   v = weights[i] * x[t] (x[t] without weights),  sf = max(amax, 2^-100) / 448
  *   with amax = max |v| over the block (sf = 1 if amax = 0; with pow2_scales
- *   rounded up to a power of two),  a[r] = e4m3_rne(clamp(v * (1/sf), -448, 448)).
+ *   rounded up to a power of two),  a[r] = e4m3_rne(v / sf),
+ * worked out to more than fp32 precision and rounded once, sf to fp32.
  *   x        bf16  [T][K] (16-byte aligned)
  *   weights  float [T][top_k] or NULL
  *   row_of, slot_of   the maps of the layout call; entries outside the range of
