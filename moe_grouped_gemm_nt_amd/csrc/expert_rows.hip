@@ -31,6 +31,7 @@ constexpr int kOneLaunch = 8192;
 constexpr int kShare = 1024;             // choices or rows per workgroup while there are workgroups to add
 constexpr int kWorkgroupsMost = 64;
 constexpr int kCopies = 2048;            // LDS words for copies of the counters
+constexpr int kCopiesMost = 8;
 
 __device__ __forceinline__ int group_of(const LayoutParams& p, int i) {
   const long long g = (long long)p.ids[i] - p.first;
@@ -62,7 +63,8 @@ __global__ __launch_bounds__(LT) void layout_count_kernel(LayoutParams p, int ch
   __syncthreads();
   for (int g = threadIdx.x; g < p.groups; g += LT) {
     int n = 0;
-    for (int c = 0; c < copies; ++c) n += lds[c * p.groups + g];
+#pragma unroll
+    for (int c = 0; c < kCopiesMost; ++c) n += c < copies ? lds[c * p.groups + g] : 0;
     counts[(size_t)blockIdx.x * p.groups + g] = n;
   }
 }
@@ -127,9 +129,10 @@ __global__ __launch_bounds__(LT) void layout_place_kernel(LayoutParams p, int ch
     int span = 0;
     if (g < G) {
       int n = 0, rest = 0;
-      for (int c = 0; c < copies; ++c) {
-        n += early[c * G + g];
-        rest += late[c * G + g];
+#pragma unroll
+      for (int c = 0; c < kCopiesMost; ++c) {
+        n += c < copies ? early[c * G + g] : 0;
+        rest += c < copies ? late[c * G + g] : 0;
       }
 #pragma unroll
       for (int w = 0; w < LW; ++w) {
@@ -220,7 +223,7 @@ hipError_t launch_layout(const LayoutParams& p, void* scratch, size_t scratch_by
   int grid = (int)((most + kShare - 1) / kShare);
   grid = grid < 1 ? 1 : (grid > kWorkgroupsMost ? kWorkgroupsMost : grid);
   int copies = kCopies / (2 * p.groups);
-  copies = copies < 1 ? 1 : (copies > 32 ? 32 : copies);
+  copies = copies < 1 ? 1 : (copies > kCopiesMost ? kCopiesMost : copies);
   int32_t* counts = nullptr;
   if (p.n > kOneLaunch && (size_t)grid * p.groups * sizeof(int32_t) <= scratch_bytes)
     counts = static_cast<int32_t*>(scratch);
