@@ -526,6 +526,7 @@ __device__ __forceinline__ uint16_t f32_bf16(float x) {
 typedef u16x8 u16x8_any __attribute__((aligned(2)));
 
 constexpr int GJ = 8;                    // rows in flight per thread
+constexpr int kMaxGridY = 65535;
 
 // Columns n..n+7 of a row (WHOLE), or its columns from n up to N, then zeros.
 template <bool WHOLE>
@@ -589,16 +590,14 @@ __device__ __forceinline__ void gather_piece(const GatherParams& p, size_t t, in
 // (8192 tokens x 8 rows of 7168: 196 us against 201 with the default one), and
 // a token's `chunks` workgroups follow one another, so that its rows' pages are
 // read whole (201 us against 206 with the tokens running fastest).
-__global__ __launch_bounds__(256) void gather_kernel(GatherParams p, int chunks) {
-  const size_t total = (size_t)p.T * chunks;
-  for (size_t i = blockIdx.x; i < total; i += gridDim.x) {
-    const size_t t = i / chunks;
-    const int n = ((int)(i - t * chunks) * blockDim.x + threadIdx.x) * 8;
-    if (n + 8 <= p.N)
-      gather_piece<true>(p, t, n);
-    else if (n < p.N)
-      gather_piece<false>(p, t, n);
-  }
+__global__ __launch_bounds__(256) void gather_kernel(GatherParams p) {
+  const size_t t = (size_t)blockIdx.z * kMaxGridY + blockIdx.y;
+  const int n = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  if (t >= (size_t)p.T) return;
+  if (n + 8 <= p.N)
+    gather_piece<true>(p, t, n);
+  else if (n < p.N)
+    gather_piece<false>(p, t, n);
 }
 
 // One workgroup per token and JG of its choices: a piece of grad_d is read once
@@ -848,9 +847,8 @@ extern "C" int dg_m_grouped_gather(const void* rows, const int32_t* row_of, cons
   // 2048 columns per workgroup, or 512 where that would leave CUs without one
   const int pieces = (int)((N + 7LL) / 8);
   const int threads = (long long)T * ((pieces + 255) / 256) >= 512 ? 256 : 64;
-  const int chunks = (pieces + threads - 1) / threads;
-  const long long items = (long long)T * chunks;
-  gather_kernel<<<(int)(items < kMaxGrid ? items : kMaxGrid), threads, 0, static_cast<hipStream_t>(stream)>>>(p, chunks);
+  const dim3 grid((pieces + threads - 1) / threads, T < kMaxGridY ? T : kMaxGridY, (T + kMaxGridY - 1) / kMaxGridY);
+  gather_kernel<<<grid, threads, 0, static_cast<hipStream_t>(stream)>>>(p);
   return launched();
 }
 
