@@ -189,8 +189,9 @@ __global__ __launch_bounds__(LT) void layout_place_kernel(LayoutParams p, int ch
     }
     __builtin_amdgcn_wave_barrier();
     if (i < we) {
-      const int row = g >= 0 ? start[g] + rank : -1;
-      const bool fits = g >= 0 && row < p.rows && (p.align || rank < p.max_m);
+      const bool in = g >= 0 && (p.align || rank < p.max_m);
+      const int row = in ? start[g] + rank : -1;
+      const bool fits = in && row < p.rows;
       if (p.row_of) p.row_of[i] = fits ? row : -1;
       if (fits) p.slot_of[row] = i;
     }
@@ -588,8 +589,8 @@ __device__ __forceinline__ void gather_piece(const GatherParams& p, size_t t, in
 // same for the whole workgroup.  Bound by the rows' bytes: GJ 16-byte loads per
 // thread are in flight before the first is summed, with the streaming policy
 // (8192 tokens x 8 rows of 7168: 196 us against 201 with the default one), and
-// a token's `chunks` workgroups follow one another, so that its rows' pages are
-// read whole (201 us against 206 with the tokens running fastest).
+// a token's workgroups follow one another, so that its rows' pages are read whole
+// (201 us against 206 with the tokens running fastest).
 __global__ __launch_bounds__(256) void gather_kernel(GatherParams p) {
   const size_t t = (size_t)blockIdx.z * kMaxGridY + blockIdx.y;
   const int n = (blockIdx.x * blockDim.x + threadIdx.x) * 8;

@@ -390,3 +390,52 @@ def test_gather_and_scatter_are_adjoint(dg):
     size = (np.abs(rows.double().numpy()) * np.abs(s)).sum()
     assert abs(left - right) <= 2.0 ** -4 * size
     assert abs(left - right) <= 5 * 2.0 ** -4 * np.sqrt((rows.double().numpy() ** 2 * s ** 2).sum())
+
+
+def test_gather_of_more_tokens_than_a_grid_axis(dg):
+    print("case: gather of 70001 tokens", flush=True)
+    rng = np.random.default_rng(6)
+    T, k, M, N = 70001, 2, 500, 9
+    rows = bf16(rng, M, N)
+    at = rng.integers(-1, M + 1, (T, k)).astype(np.int32)
+    d = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_m_grouped_gather(rows.cuda(), dev(at), None, None, d)
+    gw = torch.full((T, k), float("nan"), device="cuda")
+    dg.dg_m_grouped_gather_weight_grad(rows.cuda(), dev(at), d, gw)
+    torch.cuda.synchronize()
+    ref, mag = around.gather(rows.float().numpy(), at, None, None)
+    assert np.all(np.abs(d.float().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + (k + 1) * 2.0 ** -23 * mag + 1e-37)
+    ref, mag = around.gather_weight_grad(rows.float().numpy(), at, d.float().cpu().numpy())
+    assert np.all(np.abs(gw.cpu().numpy() - ref) <= N * 2.0 ** -24 * mag + 1e-37)
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_scatter_of_many_rows_without_room_for_the_maxima(dg, weighted):
+    # from 32768 rows on the scales are written row by row from maxima in the
+    # workspace; with a bound one too small for them, as for fewer rows: the same bits
+    print(f"case: scatter of 40064 rows with a small bound workspace, weighted={weighted}", flush=True)
+    rng = np.random.default_rng(7)
+    T, k, G, K = 10000, 4, 3, 384
+    ids = np.stack([rng.permutation(4)[:k] for _ in range(T)]).astype(np.int32)
+    x = bf16(rng, T, K).cuda()
+    w = dev(rng.standard_normal((T, k)).astype(np.float32)) if weighted else None
+    M = 40064
+    _, row_of, slot_of, _ = layout(dg, ids, 0, G, M)
+    outs = []
+    st = torch.cuda.Stream()
+    buf = torch.empty(512, dtype=torch.uint8, device="cuda")
+    for stream in (None, st):
+        a = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+        sfa = torch.zeros(K // 128, M, device="cuda")
+        torch.cuda.synchronize()
+        if stream is not None:
+            dg.dg_bind_stream_workspace(stream, buf)
+        try:
+            dg.dg_m_grouped_scatter_fp8_contiguous(x, w, row_of, slot_of, a, sfa, stream=stream)
+            torch.cuda.synchronize()
+        finally:
+            if stream is not None:
+                dg.dg_bind_stream_workspace(stream, None)
+        outs.append((a, sfa))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert int((outs[0][1] != 0).sum()) == int((slot_of >= 0).sum()) * (K // 128)

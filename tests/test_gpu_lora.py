@@ -145,3 +145,26 @@ def test_rows_without_the_adapter_do_not_see_its_values(dg):
     ref, mag = around.lora(np.nan_to_num(x.float().numpy()), np.nan_to_num(a.float().numpy()),
                            np.nan_to_num(b.float().numpy(), posinf=0), s, ids, None)
     check(got[keep], ref[keep], mag[keep], 256, 16)
+
+
+WIDE = [
+    # ranks beyond the common ones on both sides of the token count that changes the kernels
+    (20, 3, 256, 65, 512, 1, 0.1), (9, 2, 200, 70, 1152, 4, 0.0), (256, 5, 136, 33, 256, 1, 0.1),
+    (257, 5, 136, 129, 640, 1, 0.1), (600, 2, 72, 200, 384, 100, 0.2), (1500, 3, 96, 1, 128, 1, 0.0),
+    (400, 1024, 16, 20, 256, 1, 0.0), (256, 256, 8, 3, 1024, 1, 0.0), (900, 4, 256, 130, 128, 64, 0.1),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: "-".join(map(str, c)))
+def test_ranks_and_token_counts_at_the_kernels_limits(dg, case):
+    T, L, R, N, K, runs, idle = case
+    print(f"case: lora limits {case}", flush=True)
+    rng = np.random.default_rng(T * 5 + R + N)
+    x, a, b, s = problem(rng, T, L, R, N, K)
+    ids = assignment(rng, T, L, runs, idle)
+    c = bf16(rng, T, N)
+    d = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_lora_bf16_nt(x.cuda(), a.cuda(), b.cuda(), dev(s), dev(ids), c.cuda(), d)
+    torch.cuda.synchronize()
+    ref, mag = around.lora(x.float().numpy(), a.float().numpy(), b.float().numpy(), s, ids, c.float().numpy())
+    check(d.float().cpu().numpy(), ref, mag, K, R)
