@@ -11,7 +11,11 @@ namespace {
 constexpr int kMaxRank = 256;
 constexpr int THREADS = 256;
 constexpr int WAVES = THREADS / 64;
-constexpr int kInlineTokens = 256;       // up to here every workgroup finds its tile's tokens itself
+// Up to here every workgroup finds its tile's tokens itself; beyond, layout kernels
+// make lists.  Measured beside a 2112 x 7168 projection at 256 tokens against 257:
+// one adapter of rank 16 14.5 us against 16.8, 48 of them 14.9 against 18.5, 8 of
+// rank 64 22.9 against 21.1; at 128 tokens 10.0, 11.0 and 14.4 us.
+constexpr int kInlineTokens = 256;
 
 struct LoraParams {
   const uint16_t* x;
@@ -566,8 +570,12 @@ void launch_expand_listed(LoraParams p, int num_cus, hipStream_t st) {
 // K ranges: as many workgroups as run at once (three per CU with lists, by their
 // LDS; a further round for a few of them would cost as much as the others
 // together), and at least a piece for each of the four waves.
-int k_splits_for(bool listed, long long tiles, int pieces, int num_cus) {
-  const long long fit = (listed ? 3LL : 2LL) * num_cus / tiles;
+// Without lists every token has a workgroup per range, most of which may find that
+// they have no tile: no more than four of those per CU (128 tokens of 8 adapters of
+// rank 64: 14.4 us against 23.9 without this limit).
+int k_splits_for(bool listed, int tokens, long long tiles, int pieces, int num_cus) {
+  long long fit = (listed ? 3LL : 2LL) * num_cus / tiles;
+  if (!listed && fit > 4LL * num_cus / tokens) fit = 4LL * num_cus / tokens;
   const long long most = pieces / WAVES;
   const long long n = fit < most ? fit : most;
   return (int)(n < 1 ? 1 : n);
@@ -595,7 +603,7 @@ int lora_tokens(LoraParams p, const Scratch& sc, hipStream_t st) {
   if (terms) {
     const size_t one = (size_t)p.T * p.R * sizeof(float);
     if (list_bytes + one > sc.bytes) return kNoRoom;
-    int splits = k_splits_for(listed, listed ? tiles : (p.T < p.L ? p.T : p.L), pieces, sc.num_cus);
+    int splits = k_splits_for(listed, p.T, listed ? tiles : (p.T < p.L ? p.T : p.L), pieces, sc.num_cus);
     const size_t room = (sc.bytes - list_bytes) / one;
     if ((size_t)splits > room) splits = (int)room;
     p.pieces_per_split = (pieces + splits - 1) / splits;
