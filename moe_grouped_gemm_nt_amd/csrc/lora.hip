@@ -119,10 +119,6 @@ __device__ __forceinline__ bool find_item(int items, int parts, int* tile, int* 
 // time, took about 96 cycles of the CU's memory pipe per load: 97 us against 33
 // for 8192 tokens of 7168 at rank 64.)  A row's 16-byte chunk c lies at
 // c ^ swz(row).
-//
-// A tile begins its range at a piece of its own and wraps round: tokens lie K
-// values apart, and with the tiles in step the rows' same pieces would fall on a
-// few memory channels.
 __device__ __forceinline__ bf16x8 piece_operand(const uint8_t* rows, int row, int chunk) {
   return *reinterpret_cast<const bf16x8*>(rows + row * 128 + ((chunk ^ swz(row)) << 4));
 }
@@ -144,7 +140,6 @@ __global__ __launch_bounds__(THREADS) void lora_shrink_listed_kernel(LoraParams 
   const int r16 = lane & 15, g16 = lane >> 4;
   const int first = split * p.pieces_per_split;
   const int count = min(p.K / 64 - first, p.pieces_per_split);
-  const int turn = tile % count;
   const uint16_t* src[LPW];
   uint32_t dst[LPW];                           // within a slot
 #pragma unroll
@@ -159,8 +154,7 @@ __global__ __launch_bounds__(THREADS) void lora_shrink_listed_kernel(LoraParams 
   }
   const uint32_t ring0 = lds_u32(&ring[0][0]);
   auto load = [&](int i) {
-    int piece = i + turn;
-    piece = first + (piece < count ? piece : piece - count);
+    const int piece = first + i;
     const uint32_t slot = ring0 + (uint32_t)(i % RING) * (NR * 128);
 #pragma unroll
     for (int l = 0; l < LPW; ++l) dma_16(src[l] + (size_t)piece * 64, __builtin_amdgcn_readfirstlane(slot + dst[l]));
@@ -208,7 +202,6 @@ __global__ __launch_bounds__(THREADS) void lora_shrink_few_kernel(LoraParams p) 
   const int r16 = lane & 15, g16 = lane >> 4;
   const int first = split * p.pieces_per_split;
   const int count = min(p.K / 64 - first, p.pieces_per_split);
-  const int turn = tile % count;
   const int row8 = lane >> 3;
   const bool more = rows[8] >= 0;              // more than eight tokens: both halves of x
   const uint16_t *xs[2], *as[2 * RT];
@@ -228,9 +221,7 @@ __global__ __launch_bounds__(THREADS) void lora_shrink_few_kernel(LoraParams p) 
 #pragma unroll
     for (int u = 0; u < UP; ++u) {
       if (i + u * WAVES >= count) break;
-      int piece = i + u * WAVES + turn;
-      piece = first + (piece < count ? piece : piece - count);
-      const size_t k = (size_t)piece * 64;
+      const size_t k = (size_t)(first + i + u * WAVES) * 64;
       const uint32_t slot = base + u * (NR * 128);
 #pragma unroll
       for (int l = 0; l < 2 * RT; ++l) dma_16_nt(as[l] + k, __builtin_amdgcn_readfirstlane(slot + 2048 + l * 1024));
@@ -634,8 +625,10 @@ int lora_tokens(LoraParams p, const Scratch& sc, hipStream_t st) {
       launch_expand_listed<8, 1>(p, sc.num_cus, st);
   } else {
     if (terms) launch_shrink<false>(p, st);
-    // 64 columns per wave, or 16 where that would leave most of the chip without work
-    if (tiles * ((p.N + 255) / 256) >= 2 * sc.num_cus)
+    // 64 columns per wave where that makes four workgroups per CU, 16 below (2112
+    // columns, 8 adapters of rank 64: 64 tokens 10.6 us against 9.6, 128 tokens 14.5
+    // against 15.6; 48 of rank 16: 9.2 against 9.0 and 11.1 against 12.5)
+    if (tiles * ((p.N + 255) / 256) >= 4 * sc.num_cus)
       launch_expand_few<4>(p, st);
     else
       launch_expand_few<1>(p, st);
