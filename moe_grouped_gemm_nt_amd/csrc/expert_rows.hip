@@ -300,7 +300,8 @@ struct ScatterParams {
 // The block scales of many rows, row by row: sfa is laid out along the rows, and
 // written from the tokens' side each line would be touched by some 16 workgroups
 // (65536 rows of 7168: 24 us of 142).  The scatter leaves the blocks' maxima in
-// table[T][ld], and here a wave writes 64 neighbouring rows' scales.
+// table[T][ld], and here a wave writes 64 neighbouring rows' scales (10.8 us for
+// 98048 rows of 56, of which 65536 are in use).
 __global__ __launch_bounds__(256) void scatter_scales_kernel(ScatterParams p, const float* table, int ld) {
   const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= (size_t)p.rows) return;
@@ -326,7 +327,10 @@ constexpr int SJ = 8;                    // rows a thread writes per turn; also 
 // One thread per sixteen values of a token, eight threads per block of 128: the
 // token is read and quantised once and stored to all its rows (without weights;
 // with them the products are quantised per row).  In each group of eight lanes,
-// lane i also works out and stores the scale of row i of the turn.
+// lane i also works out and stores the scale of row i of the turn.  Bound by the
+// bytes: 65536 rows of 7168 from 8192 tokens take 118 us without their scales
+// (4.97 TB/s), 8192 rows from 4096 tokens 26.5 us with them (4.5 TB/s); one
+// workgroup per row, reading its token again for each, took 255 and 34.
 template <bool WEIGHTED, bool MASKED, bool TABLE>
 __global__ __launch_bounds__(256) void scatter_kernel(ScatterParams p, float* table, int ld) {
   const int per_token = p.K / 16;
@@ -603,7 +607,8 @@ __global__ __launch_bounds__(256) void gather_kernel(GatherParams p) {
 }
 
 // One workgroup per token and JG of its choices: a piece of grad_d is read once
-// for them all.
+// for them all.  Bound by the rows' bytes: 4095 tokens x 2 rows of 7165 take 36.7
+// us, 4.6 TB/s.
 template <int JG>
 __global__ __launch_bounds__(256) void gather_weight_grad_kernel(GatherParams p) {
   __shared__ float part[4][JG];

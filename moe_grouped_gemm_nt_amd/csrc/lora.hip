@@ -124,7 +124,8 @@ __device__ __forceinline__ bf16x8 piece_operand(const uint8_t* rows, int row, in
 }
 
 // Many tokens: 64 to a tile, 16 to a wave; the waves load each piece together
-// into a ring of slots, RING - 1 of them ahead of the products.
+// into a ring of slots, RING - 1 of them ahead of the products.  8192 tokens of
+// 7168 with 8 adapters of rank 64: 33 us, 3.6 TB/s of x.
 template <int RT>
 __global__ __launch_bounds__(THREADS) void lora_shrink_listed_kernel(LoraParams p) {
   constexpr int BT = kTile<true>;
@@ -188,7 +189,9 @@ __global__ __launch_bounds__(THREADS) void lora_shrink_listed_kernel(LoraParams 
 }
 
 // Few tokens: a tile of 16, whose pieces the four waves take in turn, each with
-// LDS of its own (no barrier), UP pieces at a time and all of them in flight.
+// LDS of its own (no barrier), UP pieces at a time and all of them in flight.  64
+// tokens of 48 adapters of rank 16, K 7168: 5.1 us (11 MB of A and x), of which a
+// launch is about 2.3; the rest is the chain of ids, lines and sums.
 template <int RT>
 __global__ __launch_bounds__(THREADS) void lora_shrink_few_kernel(LoraParams p) {
   constexpr int UP = RT <= 1 ? 4 : (RT <= 4 ? 2 : 1);
@@ -301,7 +304,8 @@ __device__ __forceinline__ void sum_h(const LoraParams& p, const int* rows, int 
   }
 }
 
-// Few tokens: a tile of 16, the waves side by side on 16 * NT columns each.
+// Few tokens: a tile of 16, the waves side by side on 16 * NT columns each (the
+// same call's 2112 columns: 5.2 us, latency).
 // MFMA row r of sub-tile j stands for column 4 * NT * (r / 4) + 4 * j + r % 4, so
 // that a lane's 4 * NT results are neighbours in d.
 template <int RK, int NT>
@@ -368,7 +372,9 @@ __global__ __launch_bounds__(THREADS) void lora_expand_few_kernel(LoraParams p) 
 // of a step are contiguous and come into LDS for the four waves with direct
 // loads, a step ahead; results pass through LDS so that c and d are read and
 // written in whole 128-byte lines (8 rows of 64 columns per instruction).  Bound
-// by c and d.
+// by c and d: 8192 tokens, 4096 columns, rank 64 take 38 us (3.5 TB/s of c and d),
+// 5 of them for the partial sums; with operands and results straight from and to
+// memory, in 64-byte pieces of sixteen rows, it took 78.
 template <int RK>
 __global__ __launch_bounds__(THREADS) void lora_expand_listed_kernel(LoraParams p) {
   constexpr int BT = kTile<true>;
