@@ -179,7 +179,8 @@ __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteParams p) {
 
 // Gradient: with w_j = scale * s_j (/ sum of the chosen s) and u_j = g_j * w_j,
 //   renormalised:  u_j -= (w_j / scale) * sum_i u_i
-//   sigmoid:       dx_j = u_j * (1 - s_j), 0 elsewhere   (d log sigmoid = 1 - sigmoid)
+//   sigmoid:       dx_j = u_j * sigmoid(-x_j), 0 elsewhere   (d log sigmoid(x) = 1 - sigmoid(x),
+//                  which as a difference would have no digits left for large x)
 //   softmax:       dx_i = [i chosen] u_i - p_i * sum_j u_j   (the sum is 0 when renormalised)
 // One wave per token, lane j on the j-th choice; the chosen terms go through LDS.
 template <int NI, bool BF16, bool SIGMOID>
@@ -211,12 +212,12 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
     inv = total > 0.0f ? 1.0f / total : 0.0f;
   }
   int id = -1;
-  float s = 0.0f, g = 0.0f;
+  float s = 0.0f, g = 0.0f, xi = -INFINITY;
   if (live && lane < p.top_k) {
     id = p.ids[(size_t)t * p.top_k + lane];
     if (id < 0 || id >= p.E) id = -1;
     if (id >= 0) {
-      const float xi = clean_logit(raw_logit<BF16>(p.logits, row + id));
+      xi = clean_logit(raw_logit<BF16>(p.logits, row + id));
       if (xi > -INFINITY) {
         s = SIGMOID ? sigmoid_f32(xi) : exp_f32(xi - top) * inv;
         g = p.grad_weights[(size_t)t * p.top_k + lane] * p.scale;
@@ -232,7 +233,7 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
   const float sum = wave_sum(u);
   if (p.renormalize) u -= share * sum;
   __syncthreads();
-  if (id >= 0) lds_u[wave][id] = SIGMOID ? u * (1.0f - s) : u;
+  if (id >= 0) lds_u[wave][id] = SIGMOID ? u * sigmoid_f32(-xi) : u;
   __syncthreads();
   if (!live) return;
   const float back = !SIGMOID && !p.renormalize ? sum : 0.0f;
@@ -569,7 +570,7 @@ __global__ __launch_bounds__(256) void route16_backward_kernel(RouteParams p) {
   if (p.renormalize) u -= share * sum;
   // one wave writes and reads a token's words: program order is enough
   __builtin_amdgcn_wave_barrier();
-  if (id >= 0) reinterpret_cast<float*>(&lds_u[local][0])[id] = SIGMOID ? u * (1.0f - s) : u;
+  if (id >= 0) reinterpret_cast<float*>(&lds_u[local][0])[id] = SIGMOID ? u * sigmoid_f32(-xi) : u;
   __builtin_amdgcn_wave_barrier();
   if (!live) return;
   const float back = !SIGMOID && !p.renormalize ? sum : 0.0f;
