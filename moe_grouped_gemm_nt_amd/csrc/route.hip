@@ -31,7 +31,7 @@ struct RouteParams {
 
 // e^x as 2^(x log2 e) with the product's rounding carried along: relative error
 // below 2e-7 at any x the scores use (the bare product loses |x| units of the
-// last place).  Results below 2^-126 are 0.
+// last place).  Results below 2^-126 are 0: exp_below has those.
 __device__ __forceinline__ float exp_f32(float x) {
   const float log2e = 1.44269502f, log2e_lo = 1.92596303e-8f, ln2 = 0.693147182f;
   x = fmaxf(x, -150.0f);                 // 0 from here down; also keeps lo finite
@@ -41,9 +41,31 @@ __device__ __forceinline__ float exp_f32(float x) {
   return hi < 127.0f ? fmaf(r * ln2, lo, r) : r;
 }
 
+// e^x below kLeastNormal, where the result may be subnormal, down to 2^-149: the
+// hardware's exponential and reciprocal return 0 for those, so that it is taken
+// 2^64 times as large and scaled by a product, which rounds once.
+constexpr float kLeastNormal = -87.0f;   // e^-87 is 2^-125.5
+__device__ __forceinline__ float exp_below(float x) {
+  const float log2e = 1.44269502f, log2e_lo = 1.92596303e-8f, ln2 = 0.693147182f;
+  x = fmaxf(x, -150.0f);
+  const float hi = x * log2e;
+  const float lo = fmaf(x, log2e_lo, fmaf(x, log2e, -hi));
+  const float r = __builtin_amdgcn_exp2f(hi + 64.0f);
+  return fmaf(r * ln2, lo, r) * 0x1p-64f;
+}
+// e^x of a single x <= 0
+__device__ __forceinline__ float exp_any(float x) {
+  const float r = exp_f32(x);
+  return __builtin_expect(x < kLeastNormal, 0) ? exp_below(x) : r;
+}
+
 // The hardware reciprocal (1 unit of the last place) in place of a division: the
-// scores stay within 3e-7.
+// scores stay within 3e-7.  Below kLeastNormal a sigmoid is e^x to 2^-125.
 __device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
+__device__ __forceinline__ float sigmoid_any(float x) {
+  const float r = sigmoid_f32(x);
+  return __builtin_expect(x < kLeastNormal, 0) ? exp_below(x) : r;
+}
 
 template <bool BF16>
 __device__ __forceinline__ float raw_logit(const void* p, size_t i) {
@@ -95,13 +117,13 @@ __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteParams p) {
   }
   if constexpr (SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) s[i] = sigmoid_f32(s[i]);
+    for (int i = 0; i < NI; ++i) s[i] = sigmoid_any(s[i]);
   } else {
     top = wave_max(top);
     float total = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      s[i] = s[i] > -INFINITY ? exp_f32(s[i] - top) : 0.0f;
+      s[i] = s[i] > -INFINITY ? exp_any(s[i] - top) : 0.0f;
       total += s[i];
     }
     total = wave_sum(total);
@@ -205,7 +227,7 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
     float total = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      x[i] = x[i] > -INFINITY ? exp_f32(x[i] - top) : 0.0f;
+      x[i] = x[i] > -INFINITY ? exp_any(x[i] - top) : 0.0f;
       total += x[i];
     }
     total = wave_sum(total);
@@ -219,7 +241,7 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
     if (id >= 0) {
       xi = clean_logit(raw_logit<BF16>(p.logits, row + id));
       if (xi > -INFINITY) {
-        s = SIGMOID ? sigmoid_f32(xi) : exp_f32(xi - top) * inv;
+        s = SIGMOID ? sigmoid_any(xi) : exp_any(xi - top) * inv;
         g = p.grad_weights[(size_t)t * p.top_k + lane] * p.scale;
       }
     }
@@ -233,7 +255,7 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
   const float sum = wave_sum(u);
   if (p.renormalize) u -= share * sum;
   __syncthreads();
-  if (id >= 0) lds_u[wave][id] = SIGMOID ? u * sigmoid_f32(-xi) : u;
+  if (id >= 0) lds_u[wave][id] = SIGMOID ? u * sigmoid_any(-xi) : u;
   __syncthreads();
   if (!live) return;
   const float back = !SIGMOID && !p.renormalize ? sum : 0.0f;
@@ -394,6 +416,22 @@ __device__ __forceinline__ void load16(const void* logits, size_t row, int E, in
   for (int i = 0; i < NI; ++i) x[i] = clean_logit(x[i]);
 }
 
+// y[i] = e^(x[i] - top) again where that is below the normal range, in the waves
+// that hold such a value (masked ones aside).  Counted from -inf's, the bits of a
+// finite negative number are the greater the lower it is and above all others', so
+// that one maximum finds the lowest (router of 64 tokens: 5.8 us against 6.0 with a
+// comparison per value, 5.7 with neither).
+template <int NI>
+__device__ __forceinline__ void mend_below(const float (&x)[NI], float top, float (&y)[NI]) {
+  auto mark = [](float v) { return __float_as_uint(v) - __float_as_uint(-INFINITY); };
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) most = max(most, mark(x[i] - top));
+  if (__builtin_expect(__any(most > mark(kLeastNormal)), 0))
+#pragma unroll
+    for (int i = 0; i < NI; ++i) y[i] = x[i] - top < kLeastNormal ? exp_below(x[i] - top) : y[i];
+}
+
 // y = softmax(x) of the sixteen lanes' values; top and inv, the sum's reciprocal, for single values.
 template <int NI>
 __device__ __forceinline__ void softmax16(const float (&x)[NI], float (&y)[NI], float& top, float& inv) {
@@ -407,6 +445,7 @@ __device__ __forceinline__ void softmax16(const float (&x)[NI], float (&y)[NI], 
     y[i] = x[i] > -INFINITY ? exp_f32(x[i] - top) : 0.0f;
     total += y[i];
   }
+  mend_below(x, top, y);                 // the sum is at least 1: it does not see them
   total = row_sum(total);
   inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
@@ -437,6 +476,7 @@ __global__ __launch_bounds__(256) void route16_kernel(RouteParams p) {
   if constexpr (SIGMOID) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) keys[i] = sigmoid_f32(s[i]);
+    mend_below(s, 0.0f, keys);
   } else {
     softmax16(s, keys, top, inv);
   }
@@ -517,7 +557,7 @@ __global__ __launch_bounds__(256) void route16_kernel(RouteParams p) {
   float w = 0.0f;
   if (chosen) {
     const float x = clean_logit(raw_logit<BF16>(p.logits, row + id));
-    w = SIGMOID ? sigmoid_f32(x) : exp_f32(x - top) * inv;
+    w = SIGMOID ? sigmoid_any(x) : exp_any(x - top) * inv;
   }
   if (p.renormalize) {
     const float total = row_sum(w);
@@ -559,7 +599,7 @@ __global__ __launch_bounds__(256) void route16_backward_kernel(RouteParams p) {
     load16<BF16>(p.logits, row, p.E, lane, x);
     softmax16(x, y, top, inv);
   }
-  const float s = xi > -INFINITY ? (SIGMOID ? sigmoid_f32(xi) : exp_f32(xi - top) * inv) : 0.0f;
+  const float s = xi > -INFINITY ? (SIGMOID ? sigmoid_any(xi) : exp_any(xi - top) * inv) : 0.0f;
   float share = s;                             // w_j / scale
   if (p.renormalize) {
     const float total = row_sum(s);
@@ -570,7 +610,7 @@ __global__ __launch_bounds__(256) void route16_backward_kernel(RouteParams p) {
   if (p.renormalize) u -= share * sum;
   // one wave writes and reads a token's words: program order is enough
   __builtin_amdgcn_wave_barrier();
-  if (id >= 0) reinterpret_cast<float*>(&lds_u[local][0])[id] = SIGMOID ? u * sigmoid_f32(-xi) : u;
+  if (id >= 0) reinterpret_cast<float*>(&lds_u[local][0])[id] = SIGMOID ? u * sigmoid_any(-xi) : u;
   __builtin_amdgcn_wave_barrier();
   if (!live) return;
   const float back = !SIGMOID && !p.renormalize ? sum : 0.0f;

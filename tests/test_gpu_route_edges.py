@@ -10,6 +10,7 @@ from tests.gpu_util import dev
 
 pytestmark = pytest.mark.gpu
 
+LEAST = 2.0 ** -149                                  # fp32's smallest value
 # experts, choices: the second kernel serves more than 512 experts or 16 choices
 PATHS = [(64, 4), (200, 12), (512, 16), (640, 4), (48, 20)]
 
@@ -20,6 +21,15 @@ def dg():
         pytest.skip("no GPU")
     import moe_grouped_gemm_nt_amd as m
     return m
+
+
+def run(dg, x, bias, top_k, **kw):
+    T = x.shape[0]
+    ids = torch.full((T, top_k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, top_k), float("nan"), device="cuda")
+    dg.dg_route_topk(dev(x), None if bias is None else dev(bias), ids, w, **kw)
+    torch.cuda.synchronize()
+    return ids.cpu().numpy(), w.cpu().numpy()
 
 
 def backward(dg, x, ids, g, **kw):
@@ -57,3 +67,40 @@ def test_sigmoid_gradient_keeps_its_digits_at_large_logits(dg, E, k, renorm):
     bound = np.zeros_like(ref)
     np.put_along_axis(bound, ids, 5e-6 * scale * size * rest, axis=1)
     assert np.all(np.abs(got - want) <= bound)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", PATHS)
+def test_scores_below_the_normal_range(dg, score, E, k):
+    # e^-88 .. e^-95 are subnormal numbers of fp32, 2^-127 to 2^-137: they order the
+    # choice, and their ratios are the weights
+    print(f"case: route subnormal scores {score} E={E} top_k={k}", flush=True)
+    rng = np.random.default_rng(E * 3 + k)
+    T = 18
+    x = np.stack([rng.permutation(np.linspace(-95.0, -88.0, E)) for _ in range(T)]).astype(np.float32)
+    if score == "softmax":
+        x[:, E // 3] = 0.0
+    x[-1, ::2] = -np.inf
+    for renorm in (True, False):
+        ids, w, _ = around.route(x, None, k, score, renormalize=renorm, scale=2.0)
+        got_ids, got_w = run(dg, x, None, k, score=score, renormalize=renorm, scale=2.0)
+        assert np.array_equal(got_ids, ids)
+        s = np.where(ids >= 0, around.route(x, None, k, score, renormalize=False)[1], 1.0)
+        # each score to 5e-6 of itself and a unit of the subnormal range; with their sum in the quotient twice that
+        far = 5e-6 + 2.0 * LEAST / s.min(axis=1, keepdims=True) if renorm else 5e-6 + LEAST / s
+        assert np.all(np.abs(got_w - w) <= 2.0 * far * np.abs(w) + LEAST)
+
+
+@pytest.mark.parametrize("E,k", PATHS)
+def test_sigmoid_gradient_of_subnormal_scores(dg, E, k):
+    print(f"case: sigmoid gradient of subnormal scores E={E} top_k={k}", flush=True)
+    rng = np.random.default_rng(E * 5 + k)
+    x = rng.uniform(-92.0, -88.0, (16, E)).astype(np.float32)
+    ids, _, _ = around.route(x, None, k, "sigmoid")
+    g = rng.standard_normal((16, k)).astype(np.float32)
+    got = backward(dg, x, ids, g, score="sigmoid", renormalize=True, scale=1.0)
+    ref = around.route_backward(x, ids, g, "sigmoid", True, 1.0)
+    s = np.exp(np.take_along_axis(x, ids, axis=1).astype(np.float64))
+    # a score is off by a unit of the subnormal range: its share of the sum twice that, then u's two terms
+    far = 1e-5 + 8.0 * LEAST / s.min(axis=1, keepdims=True)
+    assert np.all(np.abs(got - ref) <= far * np.abs(g).max(axis=1, keepdims=True))
