@@ -282,8 +282,9 @@ typedef enum { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_score;
  * id -1 and weight 0 in its last slots.  A logit of +inf counts as the largest
  * finite value.  Scores are fp32 values down to the subnormal ones: those below
  * 2^-149 (a sigmoid's from a logit of about -104 down) are 0, and chosen scores
- * that sum to zero give weights of zero under renormalize.  E at most 1024, top_k at most 64, num_groups at most 64
- * (DG_ERR_UNSUPPORTED otherwise); top_k <= topk_groups * E / num_groups.
+ * that sum to zero give weights of zero under renormalize.  E at most 1024,
+ * top_k at most 64, num_groups at most 64 (DG_ERR_UNSUPPORTED otherwise); top_k
+ * <= topk_groups * E / num_groups.
  * Returns a dg_status. */
 int dg_route_topk(const void* logits, int logits_type, const float* bias, int32_t* topk_ids, float* topk_weights,
                   int T, int E, int top_k, int score, int num_groups, int topk_groups, int group_top,

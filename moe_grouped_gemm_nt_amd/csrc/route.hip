@@ -280,19 +280,6 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
 // their fp32 forms here.
 constexpr int kIndexBits = 11;
 
-__device__ __forceinline__ double pack_key(float key, int e) {
-  const int rest = (1 << kIndexBits) - 1;
-  // a lower index is greater: nearer to zero for negative keys, farther for others
-  const int low = key < 0.0f ? e : rest - e;
-  const double d = (double)fminf(key + 0.0f, FLT_MAX);            // -0 is 0; +inf is finite
-  const uint64_t u = __builtin_bit_cast(uint64_t, d) | (uint64_t)low;
-  return key > -INFINITY ? __builtin_bit_cast(double, u) : -INFINITY;
-}
-__device__ __forceinline__ int key_index(double d) {
-  const int low = (int)(__builtin_bit_cast(uint64_t, d) & ((1 << kIndexBits) - 1));
-  return d < 0.0 ? low : (1 << kIndexBits) - 1 - low;
-}
-
 // max and min without the quieting of NaN that the C functions imply (keys are none)
 __device__ __forceinline__ double max_f64(double a, double b) {
   double r;
@@ -303,6 +290,19 @@ __device__ __forceinline__ double min_f64(double a, double b) {
   double r;
   asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
   return r;
+}
+
+__device__ __forceinline__ double pack_key(float key, int e) {
+  const int rest = (1 << kIndexBits) - 1;
+  // a lower index is greater: nearer to zero for negative keys, farther for others
+  const int low = key < 0.0f ? e : rest - e;
+  const double d = min_f64((double)(key + 0.0f), 0x1p128);        // -0 is 0; +inf is the next power of two
+  const uint64_t u = __builtin_bit_cast(uint64_t, d) | (uint64_t)low;
+  return key > -INFINITY ? __builtin_bit_cast(double, u) : -INFINITY;
+}
+__device__ __forceinline__ int key_index(double d) {
+  const int low = (int)(__builtin_bit_cast(uint64_t, d) & ((1 << kIndexBits) - 1));
+  return d < 0.0 ? low : (1 << kIndexBits) - 1 - low;
 }
 
 // DPP controls that pair the sixteen lanes of a row in four steps

@@ -11,6 +11,7 @@ from tests.gpu_util import dev
 pytestmark = pytest.mark.gpu
 
 LEAST = 2.0 ** -149                                  # fp32's smallest value
+MOST = float(np.finfo(np.float32).max)
 # experts, choices: the second kernel serves more than 512 experts or 16 choices
 PATHS = [(64, 4), (200, 12), (512, 16), (640, 4), (48, 20)]
 
@@ -104,3 +105,20 @@ def test_sigmoid_gradient_of_subnormal_scores(dg, E, k):
     # a score is off by a unit of the subnormal range: its share of the sum twice that, then u's two terms
     far = 1e-5 + 8.0 * LEAST / s.min(axis=1, keepdims=True)
     assert np.all(np.abs(got - ref) <= far * np.abs(g).max(axis=1, keepdims=True))
+
+
+@pytest.mark.parametrize("E,G", [(64, 1), (64, 4), (512, 8), (640, 1), (640, 20), (48, 8)])
+def test_keys_of_infinity(dg, E, G):
+    # +inf is above the largest finite key on either kernel; equal ones go to the lowest index
+    print(f"case: route keys of +inf E={E} groups={G}", flush=True)
+    x = np.tile(np.linspace(-1.0, 1.0, E, dtype=np.float32), (3, 1))
+    bias = np.zeros(E, dtype=np.float32)
+    bias[1], bias[3], bias[E - 1], bias[E - 4] = MOST, MOST, np.inf, np.inf
+    kept = max(1, G // 2)
+    for group_top in (1, 2):
+        with np.errstate(invalid="ignore"):
+            ids, w, _ = around.route(x, bias, 4, "sigmoid", G, kept, group_top)
+        assert ids[0, 0] == E - 4 and ids[0, 1] == E - 1
+        got_ids, got_w = run(dg, x, bias, 4, score="sigmoid", num_groups=G, topk_groups=kept, group_top=group_top)
+        assert np.array_equal(got_ids, ids)
+        assert np.all(np.abs(got_w - w) <= 5e-6 * w)
