@@ -86,11 +86,21 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// The sum of a group's two highest keys: as an fp32 sum, but without its range, so
+// that two keys of the lowest finite value still have a score (-inf would mask the
+// group) and two of the highest do not tie with +inf.
+__device__ __forceinline__ double group_sum(float a, float b) {
+  uint64_t u = __builtin_bit_cast(uint64_t, (double)a + (double)b);    // exact but for bits that 24 do not see
+  u += 0x0FFFFFFF + ((u >> 29) & 1);                                   // to nearest even at fp32's last place
+  return __builtin_bit_cast(double, u & ~0x1FFFFFFFull);
+}
+
 // The highest value of the wave and the lowest index that has it.
-__device__ __forceinline__ void wave_argmax(float& v, int& at) {
+template <typename F>
+__device__ __forceinline__ void wave_argmax(F& v, int& at) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
-    const float w = __shfl_xor(v, o);
+    const F w = __shfl_xor(v, o);
     const int j = __shfl_xor(at, o);
     const bool take = w > v || (w == v && j < at);
     v = take ? w : v;
@@ -149,10 +159,10 @@ __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteParams p) {
         b = fmaxf(b, fminf(a, v));
         a = fmaxf(a, v);
       }
-    float g = p.group_top > 1 && b > -INFINITY ? a + b : a;
+    const double g = p.group_top > 1 && b > -INFINITY ? group_sum(a, b) : a;
     uint64_t kept = 0;
     for (int n = 0; n < p.topk_groups; ++n) {
-      float v = (kept >> lane) & 1 || lane >= p.num_groups ? -INFINITY : g;
+      double v = (kept >> lane) & 1 || lane >= p.num_groups ? -INFINITY : g;
       int at = (kept >> lane) & 1 || lane >= p.num_groups ? INT_MAX : lane;
       wave_argmax(v, at);
       if (v == -INFINITY) break;
@@ -292,11 +302,12 @@ __device__ __forceinline__ double min_f64(double a, double b) {
   return r;
 }
 
-__device__ __forceinline__ double pack_key(float key, int e) {
+template <typename F>                    // float, or a group's score
+__device__ __forceinline__ double pack_key(F key, int e) {
   const int rest = (1 << kIndexBits) - 1;
   // a lower index is greater: nearer to zero for negative keys, farther for others
-  const int low = key < 0.0f ? e : rest - e;
-  const double d = min_f64((double)(key + 0.0f), 0x1p128);        // -0 is 0; +inf is the next power of two
+  const int low = key < F(0) ? e : rest - e;
+  const double d = min_f64((double)(key + F(0)), 0x1p130);        // -0 is 0; +inf is a finite value above all others
   const uint64_t u = __builtin_bit_cast(uint64_t, d) | (uint64_t)low;
   return key > -INFINITY ? __builtin_bit_cast(double, u) : -INFINITY;
 }
@@ -516,7 +527,8 @@ __global__ __launch_bounds__(256) void route16_kernel(RouteParams p) {
         b = fmaxf(fminf(a, c.x), fmaxf(b, c.y));
         a = fmaxf(a, c.x);
       }
-    const double g = pack_key(lane < p.num_groups ? (p.group_top > 1 && b > -INFINITY ? a + b : a) : -INFINITY, lane);
+    const double sum = p.group_top > 1 && b > -INFINITY ? group_sum(a, b) : a;
+    const double g = pack_key(lane < p.num_groups ? sum : -INFINITY, lane);
     // a group's place is the number of groups above it
     int above = 0;
     double other = g;

@@ -122,3 +122,31 @@ def test_keys_of_infinity(dg, E, G):
         got_ids, got_w = run(dg, x, bias, 4, score="sigmoid", num_groups=G, topk_groups=kept, group_top=group_top)
         assert np.array_equal(got_ids, ids)
         assert np.all(np.abs(got_w - w) <= 5e-6 * w)
+
+
+@pytest.mark.parametrize("E,G", [(64, 4), (512, 16), (640, 4), (96, 32), (30, 5)])
+def test_group_scores_beyond_the_finite_range(dg, E, G):
+    # the type's lowest value is no mask: two such keys sum to -2 MOST, which is below one of
+    # them and still a score; two of MOST are above one of them
+    print(f"case: group scores of +-2 MOST E={E} groups={G}", flush=True)
+    per, kept, k = E // G, 2, 3
+    x = np.tile(np.linspace(-1.0, 1.0, E, dtype=np.float32), (2, 1))
+    cases = []
+    low = np.full(E, -MOST, dtype=np.float32)
+    cases.append(low)                                # nothing else: the lowest indices
+    one = low.copy()                                 # the last group has one such key, the rest of it masked
+    one[(G - 1) * per + 1:] = -np.inf
+    cases.append(one)
+    high = np.zeros(E, dtype=np.float32)             # group 2 holds MOST twice, groups 0 and 1 once
+    high[0] = high[per] = high[2 * per] = high[2 * per + 1] = MOST
+    cases.append(high)
+    for at, bias in enumerate(cases):
+        ids, w, _ = around.route(x, bias, k, "sigmoid", G, kept, 2)
+        if at == 1:
+            assert ids[0].tolist() == [0, 1, 2]      # groups G - 1 and 0; equal keys by index
+            assert around.route(x, bias, 1, "sigmoid", G, 1, 2)[0][0, 0] == (G - 1) * per
+        got_ids, _ = run(dg, x, bias, k, score="sigmoid", num_groups=G, topk_groups=kept, group_top=2)
+        assert np.array_equal(got_ids, ids), at
+        ids, _, _ = around.route(x, bias, 1, "sigmoid", G, 1, 2)
+        got_ids, _ = run(dg, x, bias, 1, score="sigmoid", num_groups=G, topk_groups=1, group_top=2)
+        assert np.array_equal(got_ids, ids), at
