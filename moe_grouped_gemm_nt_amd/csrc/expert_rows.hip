@@ -3,6 +3,7 @@
 // weighted gather of their results with the gradient of its weights.
 #include "expert_rows.h"
 
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -422,7 +423,8 @@ struct KScatterParams {
 // and KR rows per thread.  The rows stay in registers between the
 // columns' maxima and the codes; one thread per column works out its scale.
 // A value times its inverse comes from pairs of fp32 (a product and its exact
-// remainder by FMA); the weighted maxima take fp64 instructions.  A row is read
+// remainder by FMA); the weighted maxima take fp64 instructions, and so do the
+// codes of a block where a product is beyond fp32's range.  A row is read
 // and written once; bound by the chain of map, row and maxima before the first
 // store: 9088 rows of 4096 columns, weighted, take 23.6 us (3.05 TB/s) in
 // workgroups of 512 threads, 24.9 in ones of 256 with 8 rows per thread.
@@ -433,6 +435,7 @@ template <bool WEIGHTED>
 __global__ __launch_bounds__(KT) void kscatter_kernel(KScatterParams p) {
   __shared__ double part[KT / 16][128];
   __shared__ float2 inverse[128];          // the sum of the two
+  __shared__ int beyond[2];                // per wave: a column's maximum has no fp32 product
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const size_t row0 = (size_t)blockIdx.y * 128;
   const int col = blockIdx.x * 128 + tx * 8;
@@ -442,16 +445,16 @@ __global__ __launch_bounds__(KT) void kscatter_kernel(KScatterParams p) {
   for (int i = 0; i < KR; ++i) slot[i] = p.slot_of[row0 + ty + KT / 16 * i];
   u16x8 h[KR];
   float w[KR];
-#pragma unroll
-  for (int i = 0; i < KR; ++i) {
-    const bool live = in && slot[i] >= 0 && slot[i] < (long long)p.T * p.top_k;
-    h[i] = u16x8{};
-    w[i] = 0.0f;                           // a row without a choice: zeros
-    if (live) {
-      h[i] = *reinterpret_cast<const u16x8*>(p.x + (size_t)(slot[i] / p.top_k) * p.N + col);
-      if constexpr (WEIGHTED) w[i] = p.weights[slot[i]];
+  auto load = [&](int s, u16x8& hs, float& ws) {
+    hs = u16x8{};
+    ws = 0.0f;                             // a row without a choice: zeros
+    if (in && s >= 0 && s < (long long)p.T * p.top_k) {
+      hs = *reinterpret_cast<const u16x8*>(p.x + (size_t)(s / p.top_k) * p.N + col);
+      if constexpr (WEIGHTED) ws = p.weights[s];
     }
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < KR; ++i) load(slot[i], h[i], w[i]);
   if constexpr (WEIGHTED) {
     double amax[8] = {};
 #pragma unroll
@@ -478,11 +481,36 @@ __global__ __launch_bounds__(KT) void kscatter_kernel(KScatterParams p) {
     const double inv = inverse_of(m, sf, p.pow2);
     const float hi = (float)inv;           // beyond fp32's range only where values below 2^-100 round to 0
     inverse[threadIdx.x] = make_float2(hi, (float)(inv - hi));
+    if constexpr (WEIGHTED) {
+      part[0][threadIdx.x] = inv;          // this thread has read its column
+      const bool any = __any(m > (double)FLT_MAX);
+      if ((threadIdx.x & 63) == 0) beyond[threadIdx.x >> 6] = any;
+    }
     const int c = blockIdx.x * 128 + threadIdx.x;
     if (c < p.N) p.sfa[(size_t)blockIdx.y * p.N + c] = sf;
   }
   __syncthreads();
   if (!in) return;
+  if constexpr (WEIGHTED) {
+    if (__builtin_expect(beyond[0] | beyond[1], 0)) {
+      // the rows again, one at a time: kept for this, they cost the others registers
+      // (weighted rows of 4096 columns: 27 us against 23)
+#pragma unroll 1
+      for (int i = 0; i < KR; ++i) {
+        const size_t row = row0 + ty + KT / 16 * i;
+        asm volatile("" ::: "memory");     // the inverses too: no register holds them from row to row
+        load(p.slot_of[row], h[0], w[0]);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (float)((double)w[0] * bf16_f32(h[0][j]) * part[0][tx * 8 + j]);
+        int2 q;
+        q.x = pack_e4m3(v[0], v[1], v[2], v[3]);
+        q.y = pack_e4m3(v[4], v[5], v[6], v[7]);
+        *reinterpret_cast<int2*>(p.a + row * p.N + col) = q;
+      }
+      return;
+    }
+  }
   float2 inv[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) inv[j] = inverse[tx * 8 + j];

@@ -7,6 +7,8 @@ import pytest
 import torch
 
 import oracle
+from oracle import around
+from tests.gpu_util import dev
 
 pytestmark = pytest.mark.gpu
 
@@ -23,6 +25,70 @@ def dg():
 
 def bf16(rng, *shape, scale=1.0):
     return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(torch.bfloat16)
+
+
+def is_nan_code(c):
+    return (c & 0x7F) == 0x7F
+
+
+def check_block_codes(codes, sf, v, amax, pow2):
+    """codes and sf of the fp64 values v with block maxima amax (sf broadcasts to v)."""
+    want = around.block_scales(amax, pow2)
+    # one rounding to fp32; a power of two is exact
+    assert np.all(np.abs(sf - want) <= (0.0 if pow2 else 2.0 ** -23) * want)
+    u = v / sf
+    q = oracle.decode_e4m3(codes).astype(np.float64)
+    # the nearest code, and the roundings of the quotient (2^-24 each) before it
+    near = 0.5 * around.e4m3_step(u) + 4 * 2.0 ** -24 * np.abs(u)
+    assert np.all(np.abs(q - np.clip(u, -448.0, 448.0)) <= near)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_kgrouped_scatter_of_products_beyond_fp32(dg, pow2):
+    # weight times value may exceed the largest fp32 value, and their scale not: 1.5e41 / 448 is
+    # the most; columns with such a product beside ordinary ones
+    print(f"case: K-grouped scatter of products up to 1e41, pow2={pow2}", flush=True)
+    rng = np.random.default_rng(11)
+    T, N = 300, 160
+    x = rng.standard_normal((T, N)).astype(np.float32)
+    x[:, ::3] *= np.float32(2.0 ** 126)
+    x = torch.from_numpy(np.clip(x, -3e38, 3e38)).to(torch.bfloat16)
+    w = (rng.random((T, 1)) * 100.0 + 1.0).astype(np.float32)
+    w[5::7] *= np.float32(1e-3)
+    K = 384
+    slot = np.full(K, -1, dtype=np.int32)
+    slot[:T] = rng.permutation(T)
+    a = torch.full((K, N), KEEP, dtype=torch.uint8, device="cuda")
+    sfa = torch.full((K // 128, N), -3.0, device="cuda")
+    dg.dg_k_grouped_scatter_fp8(x.cuda(), dev(w), dev(slot), 1, a, sfa, pow2_scales=pow2)
+    torch.cuda.synchronize()
+    v = np.where(slot[:, None] >= 0, x.double().numpy()[slot] * w.astype(np.float64)[slot], 0.0).reshape(K // 128, 128, N)
+    amax = np.abs(v).max(axis=1)
+    assert amax.max() > 3.5e38 and amax.max() < 1.4e41
+    codes = a.cpu().numpy()
+    assert not is_nan_code(codes).any()
+    check_block_codes(codes.reshape(v.shape), sfa.cpu().numpy().astype(np.float64)[:, None, :], v, amax[:, None, :], pow2)
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_kgrouped_scatter_of_nonfinite_values(dg, weighted):
+    # as in the M-grouped forms: a NaN keeps to its place, an infinity makes its block's scale infinite
+    print(f"case: K-grouped scatter of NaN and infinities, weighted={weighted}", flush=True)
+    x = torch.ones(4, 32, dtype=torch.bfloat16)
+    x[0, 3], x[1, 5], x[2, 9] = float("nan"), float("inf"), float("-inf")
+    x[:, 20] = float("nan")
+    slot = np.full(128, -1, dtype=np.int32)
+    slot[[0, 7, 64, 127]] = [0, 1, 2, 3]
+    w = torch.full((4, 1), 2.0, device="cuda") if weighted else None
+    a = torch.zeros(128, 32, dtype=torch.uint8, device="cuda")
+    sfa = torch.zeros(1, 32, device="cuda")
+    dg.dg_k_grouped_scatter_fp8(x.cuda(), w, dev(slot), 1, a, sfa)
+    torch.cuda.synchronize()
+    c, s = a.cpu().numpy(), sfa.cpu().numpy()[0]
+    nan = is_nan_code(c)
+    assert nan[0, 3] and nan[7, 5] and nan[64, 9] and nan[[0, 7, 64, 127], 20].all() and nan.sum() == 7
+    assert np.isinf(s[[5, 9]]).all() and s[20] == 1.0 and s[3] == np.float32((2.0 if weighted else 1.0) / 448.0)
+    assert np.all(c[[7, 64, 127], 3] == 0x7E) and np.all(c[1:7] == 0) and np.all(c[[0, 64, 127], 5] == 0)
 
 
 def exact_codes(x, amax):
