@@ -430,6 +430,7 @@ struct KScatterParams {
 // workgroups of 512 threads, 24.9 in ones of 256 with 8 rows per thread.
 constexpr int KT = 512;                  // threads per workgroup
 constexpr int KR = 128 * 16 / KT;        // rows per thread
+constexpr int kMaxGridY = 65535;         // a grid's second axis; what is beyond goes on the third
 
 template <bool WEIGHTED>
 __global__ __launch_bounds__(KT) void kscatter_kernel(KScatterParams p) {
@@ -437,7 +438,9 @@ __global__ __launch_bounds__(KT) void kscatter_kernel(KScatterParams p) {
   __shared__ float2 inverse[128];          // the sum of the two
   __shared__ int beyond[2];                // per wave: a column's maximum has no fp32 product
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const size_t row0 = (size_t)blockIdx.y * 128;
+  const size_t block = (size_t)blockIdx.z * kMaxGridY + blockIdx.y;
+  if (block >= (size_t)p.K / 128) return;
+  const size_t row0 = block * 128;
   const int col = blockIdx.x * 128 + tx * 8;
   const bool in = col < p.N;               // N % 16 == 0: whole 8-column pieces
   int slot[KR];
@@ -487,7 +490,7 @@ __global__ __launch_bounds__(KT) void kscatter_kernel(KScatterParams p) {
       if ((threadIdx.x & 63) == 0) beyond[threadIdx.x >> 6] = any;
     }
     const int c = blockIdx.x * 128 + threadIdx.x;
-    if (c < p.N) p.sfa[(size_t)blockIdx.y * p.N + c] = sf;
+    if (c < p.N) p.sfa[block * p.N + c] = sf;
   }
   __syncthreads();
   if (!in) return;
@@ -560,7 +563,6 @@ __device__ __forceinline__ uint16_t f32_bf16(float x) {
 typedef u16x8 u16x8_any __attribute__((aligned(2)));
 
 constexpr int GJ = 8;                    // rows in flight per thread
-constexpr int kMaxGridY = 65535;
 
 // Columns n..n+7 of a row (WHOLE), or its columns from n up to N, then zeros.
 template <bool WHOLE>
@@ -852,10 +854,10 @@ extern "C" int dg_k_grouped_scatter_fp8(const void* x, const float* weights, con
   if (!aligned(x, 16) || !aligned(a, 16)) return fail(DG_ERR_INVALID_ARG, "x and a must be 16-byte aligned");
   if (!aligned(sfa, 4) || !aligned(weights, 4) || !aligned(slot_of, 4))
     return fail(DG_ERR_INVALID_ARG, "sfa, weights and slot_of must be 4-byte aligned");
-  if (K / 128 > 65535) return fail(DG_ERR_UNSUPPORTED, "K=%d exceeds %d rows", K, 65535 * 128);
   KScatterParams p{static_cast<const uint16_t*>(x), weights, slot_of, static_cast<uint8_t*>(a), sfa, T, top_k, K, N,
                    pow2_scales != 0};
-  const dim3 grid((N + 127) / 128, K / 128);
+  const int blocks = K / 128;
+  const dim3 grid((N + 127) / 128, blocks < kMaxGridY ? blocks : kMaxGridY, (blocks + kMaxGridY - 1) / kMaxGridY);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (weights)
     kscatter_kernel<true><<<grid, KT, 0, st>>>(p);

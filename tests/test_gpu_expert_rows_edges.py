@@ -91,6 +91,27 @@ def test_kgrouped_scatter_of_nonfinite_values(dg, weighted):
     assert np.all(c[[7, 64, 127], 3] == 0x7E) and np.all(c[1:7] == 0) and np.all(c[[0, 64, 127], 5] == 0)
 
 
+def test_kgrouped_scatter_of_more_blocks_than_a_grid_axis(dg):
+    print("case: K-grouped scatter of 65539 blocks of rows", flush=True)
+    rng = np.random.default_rng(12)
+    K, N, T = 65539 * 128, 32, 6
+    x = bf16(rng, T, N)
+    rows = torch.tensor([0, 65534 * 128 + 127, 65535 * 128, 65536 * 128 + 5, K - 129, K - 1])
+    slot = torch.full((K,), -1, dtype=torch.int32)
+    slot[rows] = torch.arange(T, dtype=torch.int32)
+    a = torch.full((K, N), KEEP, dtype=torch.uint8, device="cuda")
+    sfa = torch.full((K // 128, N), -3.0, device="cuda")
+    dg.dg_k_grouped_scatter_fp8(x.cuda(), None, slot.cuda(), 1, a, sfa)
+    torch.cuda.synchronize()
+    block = torch.div(rows, 128, rounding_mode="floor")
+    assert len(set(block.tolist())) == T                  # one row each: its own maximum
+    v = x.double().numpy()
+    check_block_codes(a[rows.cuda()].cpu().numpy(), sfa[block.cuda()].cpu().numpy().astype(np.float64), v, np.abs(v), False)
+    assert int((a != 0).any(1).sum()) == T
+    sfa[block.cuda()] = 1.0
+    assert bool((sfa == 1.0).all())                       # blocks without a choice
+
+
 def exact_codes(x, amax):
     """e4m3 values of x * 448 / amax rounded to nearest even, in whole numbers: x bf16 values and amax
     bf16 values > 0, fp64 arrays that broadcast; also where a quotient lies halfway between two codes."""
