@@ -37,8 +37,9 @@
  * on the device.  Faults inside a kernel surface at the caller's next
  * synchronisation, as for any HIP kernel.
  *
- * All calls on one device share its split-K workspace (fp32 partial tiles)
- * and its scale-check results, unless their stream has a workspace of its own
+ * All calls on one device share its workspace (split-K partial tiles, and the
+ * scratch of the operators around the products) and its scale-check results,
+ * unless their stream has a workspace of its own
  * (dg_bind_stream_workspace).  Calls enqueued on one stream, or ordered across
  * streams by events, are safe; calls that may run at the same time on
  * different streams of one device race on the shared memory and must be
@@ -216,22 +217,25 @@ int dg_choose_config(int form, int rows, int N, int K, int num_groups, int num_c
                      int has_c, int* cfg, int* splits);
 
 /* Binds a caller-owned device workspace to a stream of the current device:
- * every later call of this library enqueued on that stream uses it in place
- * of the device's shared workspace (split-K partial tiles and scale-check
- * verdicts), so that calls running at the same time on different streams no
- * longer share scratch memory.  workspace: device memory on the current
- * device, 256-byte aligned, at least 256 bytes (the verdicts).  A workspace of
- * at least 256 + 4096 bytes also holds, after the verdicts, the 4096 bytes of
- * counters of the one-launch decode configuration, which this call clears
- * (synchronously) and every later call leaves at zero; the rest holds
- * partials, and the configuration is chosen so that they fit (a bound
- * workspace of a few hundred bytes simply means no split-K).  The caller keeps
- * the memory alive, and unused by anything else, while the binding lasts and
- * while calls enqueued with it run.  workspace NULL (or bytes 0) removes the
- * stream's binding.  The allocation-free call (dg_fp8_gemm_nt_noalloc) always
- * uses its own fixed array.  Returns DG_ERR_INVALID_ARG for a misaligned or
- * too small workspace, DG_ERR_HIP if the current device cannot be queried or
- * the counters cannot be cleared. */
+ * every later call of this library enqueued on that stream uses it in place of
+ * the device's shared workspace (split-K partial tiles and scale-check
+ * verdicts; and what the operators around the products put there: the layouts'
+ * counts, the scatters' block maxima, the adapters' lists and partial sums), so
+ * that calls running at the same time on different streams no longer share
+ * scratch memory. workspace: device memory on the current device, 256-byte
+ * aligned, at least 256 bytes (the verdicts). A workspace of at least 256 +
+ * 4096 bytes also holds, after the verdicts, the 4096 bytes of counters of the
+ * one-launch decode configuration, which this call clears (synchronously) and
+ * every later call leaves at zero; the rest holds partials, and the
+ * configuration is chosen so that they fit (a bound workspace of a few hundred
+ * bytes simply means no split-K, and one launch for a layout or a scatter; the
+ * adapters refuse one without room for 16 tokens). The caller keeps the memory
+ * alive, and unused by anything else, while the binding lasts and while calls
+ * enqueued with it run. workspace NULL (or bytes 0) removes the stream's
+ * binding. The allocation-free call (dg_fp8_gemm_nt_noalloc) always uses its
+ * own fixed array. Returns DG_ERR_INVALID_ARG for a misaligned or too small
+ * workspace, DG_ERR_HIP if the current device cannot be queried or the counters
+ * cannot be cleared. */
 int dg_bind_stream_workspace(void* stream, void* workspace, size_t bytes);
 
 /* Host-side check of a contiguous grouped_layout held in HOST memory (M int32
@@ -328,6 +332,7 @@ int dg_m_grouped_layout_contiguous(const int32_t* topk_ids, int T, int top_k, in
  * max_m have none.
  *   masked_m int32 [num_groups]  min(choices, max_m) per local expert
  *   row_of   int32 [T][top_k], slot_of int32 [num_groups][max_m]   as above
+ * num_groups at most 1024.  Scratch: workspace (a small one costs speed only).
  * Returns a dg_status. */
 int dg_m_grouped_layout_masked(const int32_t* topk_ids, int T, int top_k, int first_expert, int num_groups, int max_m,
                                int32_t* masked_m, int32_t* row_of, int32_t* slot_of, void* stream);

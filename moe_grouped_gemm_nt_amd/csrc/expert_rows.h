@@ -25,8 +25,8 @@ struct LayoutParams {
   int others;              // nonzero: choices outside the first groups - 1 ids form the last group
 };
 
-// Enqueues the layout kernels; `scratch` may be too small for more than one
-// workgroup's counts (then one workgroup does the whole layout).
+// Enqueues the layout kernels; `scratch` may be too small for the workgroups'
+// counts (then every workgroup counts all the choices itself, in one launch).
 hipError_t launch_layout(const LayoutParams& p, void* scratch, size_t scratch_bytes, hipStream_t stream);
 
 }  // namespace dg

@@ -27,6 +27,10 @@ def bf16(rng, *shape, scale=1.0):
     return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(torch.bfloat16)
 
 
+def i32(*shape, fill=-9):
+    return torch.full(shape, fill, dtype=torch.int32, device="cuda")
+
+
 def is_nan_code(c):
     return (c & 0x7F) == 0x7F
 
@@ -110,6 +114,53 @@ def test_kgrouped_scatter_of_more_blocks_than_a_grid_axis(dg):
     assert int((a != 0).any(1).sum()) == T
     sfa[block.cuda()] = 1.0
     assert bool((sfa == 1.0).all())                       # blocks without a choice
+
+
+@pytest.mark.parametrize("ws", [0, 4096, 1 << 20])
+def test_masked_layout_with_a_bound_workspace(dg, ws):
+    print(f"case: masked layout on a stream with a workspace of {256 + ws} bytes", flush=True)
+    rng = np.random.default_rng(14)
+    T, k, G, max_m = 9000, 4, 64, 500
+    ids = np.stack([rng.permutation(G)[:k] for _ in range(T)]).astype(np.int32)
+    st = torch.cuda.Stream()
+    buf = torch.zeros(256 + ws, dtype=torch.uint8, device="cuda")
+    dg.dg_bind_stream_workspace(st, buf)
+    try:
+        out = i32(G), i32(T, k), i32(G, max_m)
+        d = dev(ids)
+        torch.cuda.synchronize()
+        dg.dg_m_grouped_layout_masked(d, 0, *out, stream=st)
+        st.synchronize()
+    finally:
+        dg.dg_bind_stream_workspace(st, None)
+    for g, r in zip(out, around.layout_masked(ids, 0, G, max_m)):
+        assert np.array_equal(g.cpu().numpy(), r)
+
+
+def test_masked_layouts_on_two_streams(dg):
+    # more than 8192 choices: the counts go through each stream's own workspace
+    print("case: masked layouts on two streams at once", flush=True)
+    rng = np.random.default_rng(15)
+    T, k, G, max_m = 20000, 4, 96, 1200
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.empty(1 << 20, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ids = [rng.integers(0, G, (T, k)).astype(np.int32) for _ in range(2)]
+    d_ids = [dev(v) for v in ids]
+    outs = [(i32(G), i32(T, k), i32(G, max_m)) for _ in range(2)]
+    torch.cuda.synchronize()
+    try:
+        for s, b in zip(streams, spaces):
+            dg.dg_bind_stream_workspace(s, b)
+        for _ in range(10):
+            for s, v, o in zip(streams, d_ids, outs):
+                dg.dg_m_grouped_layout_masked(v, 0, *o, stream=s)
+        torch.cuda.synchronize()
+    finally:
+        for s in streams:
+            dg.dg_bind_stream_workspace(s, None)
+    for v, o in zip(ids, outs):
+        for g, r in zip(o, around.layout_masked(v, 0, G, max_m)):
+            assert np.array_equal(g.cpu().numpy(), r)
 
 
 def exact_codes(x, amax):
