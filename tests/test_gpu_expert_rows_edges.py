@@ -116,6 +116,67 @@ def test_kgrouped_scatter_of_more_blocks_than_a_grid_axis(dg):
     assert bool((sfa == 1.0).all())                       # blocks without a choice
 
 
+WGRAD = [
+    # T, top_k, M, N: from 512 tokens on and more than two choices, eight to a workgroup
+    (512, 3, 700, 129), (513, 8, 900, 2047), (700, 11, 400, 520), (600, 64, 300, 77), (2050, 4, 1000, 4096), (900, 9, 50, 3),
+]
+
+
+@pytest.mark.parametrize("shape", WGRAD, ids=str)
+def test_gather_weight_gradient_by_eights(dg, shape):
+    T, k, M, N = shape
+    print(f"case: gather weight gradient {shape}", flush=True)
+    rng = np.random.default_rng(N + T)
+    rows, g = bf16(rng, M, N), bf16(rng, T, N)
+    at = rng.integers(0, M, (T, k)).astype(np.int32)
+    at[rng.random((T, k)) < 0.2] = -1
+    at[0, -1] = M
+    at[1] = -1
+    at[2, :-1] = -1
+    out = torch.full((T, k), float("nan"), device="cuda")
+    dg.dg_m_grouped_gather_weight_grad(rows.cuda(), dev(at), g.cuda(), out)
+    torch.cuda.synchronize()
+    ref, mag = around.gather_weight_grad(rows.float().numpy(), at, g.float().numpy())
+    # products of bf16 are exact in fp32; N additions in any order
+    assert np.all(np.abs(out.cpu().numpy() - ref) <= N * 2.0 ** -24 * mag + 1e-37)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_masked_scatter_into_many_rows(dg, weighted, pow2):
+    # from 32768 rows on the scales are written row by row, here into [G][K/128][max_m]
+    G, max_m, T, k, K = 130, 300, 700, 3, 384
+    print(f"case: masked scatter into {G} x {max_m} rows, weighted={weighted} pow2={pow2}", flush=True)
+    rng = np.random.default_rng(13)
+    ids = np.stack([rng.permutation(G)[:k] for _ in range(T)]).astype(np.int32)
+    ids[:400, 0] = 7                                      # one expert runs over
+    ids[:400, 1:] = np.stack([rng.permutation(G - 8)[:k - 1] + 8 for _ in range(400)])
+    x = bf16(rng, T, K)
+    w = (rng.random((T, k)).astype(np.float32) - 0.3) if weighted else None
+    masked_m, row_of, slot_of = i32(G), i32(T, k), i32(G, max_m)
+    dg.dg_m_grouped_layout_masked(dev(ids), 0, masked_m, row_of, slot_of)
+    a = torch.full((G, max_m, K), KEEP, dtype=torch.uint8, device="cuda")
+    sfa = torch.full((G, K // 128, max_m), -3.0, device="cuda")
+    dg.dg_m_grouped_scatter_fp8_masked(x.cuda(), None if w is None else dev(w), row_of, slot_of, a, sfa, pow2_scales=pow2)
+    torch.cuda.synchronize()
+    want_m, want_row, want_slot = around.layout_masked(ids, 0, G, max_m)
+    assert np.array_equal(slot_of.cpu().numpy(), want_slot) and np.array_equal(row_of.cpu().numpy(), want_row)
+    assert np.array_equal(masked_m.cpu().numpy(), want_m) and want_m[7] == max_m
+    codes = a.cpu().numpy().reshape(G * max_m, K)
+    sf = sfa.cpu().numpy().transpose(0, 2, 1).reshape(G * max_m, K // 128).astype(np.float64)
+    slot = want_slot.ravel()
+    assert np.all(codes[slot < 0] == KEEP) and np.all(sf[slot < 0] == -3.0)
+    rows = np.nonzero(slot >= 0)[0]
+    v = x.double().numpy()[slot[rows] // k]
+    if weighted:
+        v = v * w.astype(np.float64).ravel()[slot[rows], None]
+    v = v.reshape(rows.size, K // 128, 128)
+    amax = np.abs(v).max(axis=2)
+    if pow2:                     # the power is chosen from the fp32 quotient
+        amax = (amax / 448.0).astype(np.float32).astype(np.float64) * 448.0
+    check_block_codes(codes[rows].reshape(v.shape), sf[rows][:, :, None], v, amax[:, :, None], pow2)
+
+
 @pytest.mark.parametrize("ws", [0, 4096, 1 << 20])
 def test_masked_layout_with_a_bound_workspace(dg, ws):
     print(f"case: masked layout on a stream with a workspace of {256 + ws} bytes", flush=True)
