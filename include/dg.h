@@ -400,7 +400,7 @@ int dg_m_grouped_gather_weight_grad(const void* rows, const int32_t* row_of, con
  *   scales float [num_adapters] or NULL (1), adapter_ids int32 [T]
  *   c  bf16 [T] rows of N values, ldc apart, or NULL (0); may equal d
  *   d  bf16 [T] rows of N values, ldd apart
- * A . x is summed in fp32 and kept to 16 bits of mantissa or more.  K must be a
+ * A . x is summed, scaled and multiplied with B in fp32.  K must be a
  * multiple of 128, R a multiple of 8 and at most 256 (adapters of lower rank are
  * filled up with zeros); any N.  num_adapters at most 1024 (DG_ERR_UNSUPPORTED
  * otherwise).  Scratch: workspace (DG_ERR_UNSUPPORTED if a bound one has no room

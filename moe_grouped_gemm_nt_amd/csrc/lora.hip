@@ -39,7 +39,6 @@ struct LoraParams {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 
 // Two shapes of workgroup.  LISTED (many tokens): a tile of 64 tokens from the
 // layout kernels' lists, 16 to a wave.  Otherwise (few tokens): a tile of 16, the
@@ -278,10 +277,10 @@ struct Piece {
 
 // ---- d = c + B . h -----------------------------------------------------------
 // Again transposed: MFMA rows are columns of d.  h (the K ranges' sum times the
-// adapter's scale) is split into two bf16, h = hi + lo to 16 bits, and both
-// halves are multiplied: the products with B are then exact to 2^-17.
+// adapter's scale) stays fp32 in LDS and is multiplied as three bf16 that add up
+// to it, so that differences of ranks in B keep its last bits.
 template <int BT, int RP>
-__device__ __forceinline__ void sum_h(const LoraParams& p, const int* rows, int id, uint16_t (*hs)[BT][RP + 8]) {
+__device__ __forceinline__ void sum_h(const LoraParams& p, const int* rows, int id, float (*hs)[RP + 4]) {
   const float scale = p.scales ? p.scales[id] : 1.0f;
   for (int i = threadIdx.x; i < BT * (RP / 4); i += THREADS) {
     const int at = i / (RP / 4), r = i % (RP / 4) * 4;
@@ -291,16 +290,24 @@ __device__ __forceinline__ void sum_h(const LoraParams& p, const int* rows, int 
 #pragma unroll 4
       for (int s = 0; s < p.k_splits; ++s)
         h += *reinterpret_cast<const f32x4*>(p.partial + ((size_t)s * p.T + t) * p.R + r);
-    u16x4 hi, lo;
+    *reinterpret_cast<f32x4*>(&hs[at][r]) = h * scale;
+  }
+}
+
+// Eight neighbouring values of h as MFMA operands, v = part[0] + part[1] + part[2]
+// (an infinity or a NaN is part[0] alone).
+constexpr int kParts = 3;
+__device__ __forceinline__ void split_h(const float* h, bf16x8 (&part)[kParts]) {
+  const f32x4 h0 = *reinterpret_cast<const f32x4*>(h), h1 = *reinterpret_cast<const f32x4*>(h + 4);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v = h[e] * scale;
-      hi[e] = f32_to_bf16(v);
-      const float back = bf16_to_f32(hi[e]);
-      lo[e] = fabsf(back) < INFINITY ? f32_to_bf16(v - back) : 0;
+  for (int e = 0; e < 8; ++e) {
+    float rest = e < 4 ? h0[e] : h1[e - 4];
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+      part[q][e] = static_cast<__bf16>(rest);
+      const float back = static_cast<float>(part[q][e]);
+      rest = fabsf(back) < INFINITY ? rest - back : 0.0f;
     }
-    *reinterpret_cast<u16x4*>(&hs[0][at][r]) = hi;
-    *reinterpret_cast<u16x4*>(&hs[1][at][r]) = lo;
   }
 }
 
@@ -311,11 +318,10 @@ __device__ __forceinline__ void sum_h(const LoraParams& p, const int* rows, int 
 template <int RK, int NT>
 __global__ __launch_bounds__(THREADS) void lora_expand_few_kernel(LoraParams p) {
   constexpr int RP = RK * 32;             // ranks padded to whole MFMA steps
-  constexpr int LD = RP + 8;              // LDS row: 16 bytes on, so that 16 rows start in different banks
   constexpr int NE = 4 * NT;
   typedef typename Piece<NE>::U U;
   __shared__ int rows[16];
-  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][LD];
+  __shared__ __attribute__((aligned(16))) float hs[16][RP + 4];
   int id, tile, part;
   if (!find_item<false>(p.tiles * p.parts, p.parts, &tile, &part)) return;
   if (!find_tile<false>(p, tile, rows, &id)) return;
@@ -342,13 +348,15 @@ __global__ __launch_bounds__(THREADS) void lora_expand_few_kernel(LoraParams p) 
     sum_h<16, RP>(p, rows, id, hs);
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < RK; ++k)
+    for (int k = 0; k < RK; ++k) {
+      bf16x8 h[kParts];
+      split_h(&hs[r16][k * 32 + g16 * 8], h);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const bf16x8 h = *reinterpret_cast<const bf16x8*>(&hs[q][r16][k * 32 + g16 * 8]);
+      for (int q = 0; q < kParts; ++q)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][k], h, acc[j], 0, 0, 0);
-      }
+        for (int j = 0; j < NT; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][k], h[q], acc[j], 0, 0, 0);
+    }
   }
   if (token < 0 || n >= p.N) return;
   uint16_t* d = p.d + (size_t)token * p.ldd + n;
@@ -382,7 +390,7 @@ __global__ __launch_bounds__(THREADS) void lora_expand_listed_kernel(LoraParams 
   constexpr int OLD = 68;                 // a row of results in LDS: 64 and 16 bytes on
   typedef typename Piece<8>::U U;
   union Shared {
-    uint16_t hs[2][BT][RP + 8];
+    float hs[BT][RP + 4];
     float out[WAVES][16][OLD];
   };
   __shared__ int rows[BT];
@@ -461,12 +469,9 @@ __global__ __launch_bounds__(THREADS) void lora_expand_listed_kernel(LoraParams 
   load_c(0);
   sum_h<BT, RP>(p, rows, id, sh.hs);
   __syncthreads();
-  bf16x8 hf[RK][2];
+  bf16x8 hf[RK][kParts];
 #pragma unroll
-  for (int k = 0; k < RK; ++k)
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      hf[k][q] = *reinterpret_cast<const bf16x8*>(&sh.hs[q][wave * 16 + r16][k * 32 + g16 * 8]);
+  for (int k = 0; k < RK; ++k) split_h(&sh.hs[wave * 16 + r16][k * 32 + g16 * 8], hf[k]);
   for (int step = 0; step < count; ++step) {
     // this step's B is complete: only the last step's stores, issued after it, may
     // be under way; and every wave has left the other slot and, at first, hs
@@ -491,8 +496,8 @@ __global__ __launch_bounds__(THREADS) void lora_expand_listed_kernel(LoraParams 
         bf16x8 bf = {};
         if (chunk < row_chunks)
           bf = *reinterpret_cast<const bf16x8*>(slot + (row * row_chunks + (chunk ^ (row & turn))) * 16);
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf, hf[k][0], acc[j], 0, 0, 0);
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf, hf[k][1], acc[j], 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf, hf[k][q], acc[j], 0, 0, 0);
       }
     // a wave's own rows: program order is enough
 #pragma unroll

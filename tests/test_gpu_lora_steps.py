@@ -97,3 +97,26 @@ def test_sixty_four_columns_per_wave(dg, case, mode):
     print(f"case: lora wide columns {case} c={mode}", flush=True)
     assert T * ((N + 255) // 256) >= 4 * 256
     run_case(dg, *case, mode, T * 3 + R)
+
+
+@pytest.mark.parametrize("T", [1, 16, 200, 300, 900])
+@pytest.mark.parametrize("R", [8, 40, 64, 128, 256])
+def test_the_inner_product_keeps_its_fp32_digits(dg, T, R):
+    # A x is 1 + 2^-9 + t 2^-20 at rank t and B takes the difference of two ranks: what is left
+    # is the last digits, exact in fp32 and in bf16
+    print(f"case: lora differences of ranks, {T} tokens of rank {R}", flush=True)
+    K, N = 128, 48
+    x = torch.ones(T, K, dtype=torch.bfloat16)
+    a = torch.zeros(1, R, K)
+    a[0, :, 0], a[0, :, 40], a[0, :, 127] = 1.0, 2.0 ** -9, torch.arange(R) * 2.0 ** -20
+    b = torch.zeros(1, N, R)
+    for n in range(N):
+        b[0, n, (3 * n + 1) % R] += 1.0
+        b[0, n, (5 * n) % R] -= 1.0
+    a, b = a.to(torch.bfloat16), b.to(torch.bfloat16)
+    d = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_lora_bf16_nt(x.cuda(), a.cuda(), b.cuda(), None, torch.zeros(T, dtype=torch.int32, device="cuda"), None, d)
+    torch.cuda.synchronize()
+    ref = ((x.double() @ a[0].double().t()) @ b[0].double().t()).numpy()
+    assert np.abs(ref).max() > 0
+    assert np.array_equal(d.float().cpu().numpy(), ref)
