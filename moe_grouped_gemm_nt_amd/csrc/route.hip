@@ -713,8 +713,7 @@ void launch_score(const RouteParams& p, int score, int grid, hipStream_t st) {
 }
 
 template <bool BACK>
-int launch_route(const RouteParams& p, int logits_type, int score, hipStream_t st) {
-  const bool bf = logits_type == DG_BF16;
+int launch_tokens(const RouteParams& p, bool bf, int score, hipStream_t st) {
   if (!BACK && fits_route16(p)) {
     if (p.E <= 64)
       launch_route16<4, 4>(p, bf, score, st);
@@ -751,6 +750,31 @@ int launch_route(const RouteParams& p, int logits_type, int score, hipStream_t s
 #undef DG_ROUTE_CASE
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+  return DG_OK;
+}
+
+// A grid has fewer than 2^32 threads (a launch of more is cut short without an
+// error): at 64 to a token, this many tokens per launch.
+constexpr int kTokensPerLaunch = 1 << 25;
+
+template <bool BACK>
+int launch_route(RouteParams p, int logits_type, int score, hipStream_t st) {
+  const bool bf = logits_type == DG_BF16;
+  const int T = p.T;
+  for (int t = 0; t < T; t += p.T) {
+    p.T = T - t < kTokensPerLaunch ? T - t : kTokensPerLaunch;
+    const int s = launch_tokens<BACK>(p, bf, score, st);
+    if (s != DG_OK) return s;
+    const size_t logits = (size_t)p.T * p.E * (bf ? 2 : 4), choices = (size_t)p.T * p.top_k;
+    p.logits = static_cast<const uint8_t*>(p.logits) + logits;
+    p.ids += choices;
+    if constexpr (BACK) {
+      p.grad_weights += choices;
+      p.grad_logits = static_cast<uint8_t*>(p.grad_logits) + logits;
+    } else {
+      p.weights += choices;
+    }
+  }
   return DG_OK;
 }
 
