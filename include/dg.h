@@ -261,7 +261,8 @@ int dg_check_grouped_layout(const int32_t* grouped_layout, int M, int num_groups
  * dense projection.  They follow the rules above: device pointers owned by the
  * caller, checks on the host, no synchronisation, capturable in a HIP graph
  * after dg_init(), and the device's (or the stream's bound) workspace as
- * scratch where a call says so.  An array of no elements may be NULL.
+ * scratch where a call says so.  An array of no elements may be NULL.  T * top_k
+ * at most 2^30 in all calls but the router's.
  *
  * Sums, softmax statistics and scales are fp32; bf16 results are rounded once
  * (to nearest, ties to even).  No result depends on the order of atomics. */
@@ -365,8 +366,8 @@ int dg_m_grouped_scatter_fp8_masked(const void* x, const float* weights, const i
  *   x bf16 [T][N] (16-byte aligned), weights float [T][top_k] or NULL,
  *   slot_of int32 [K], a uint8 [K][N] (16-byte aligned), sfa float [K/128][N]
  * K (the rows, a multiple of 128) may be less than the layout's M: the segments
- * used.  N must be a multiple of 16 (DG_ERR_UNSUPPORTED otherwise).  Returns a
- * dg_status. */
+ * used.  N must be a multiple of 16 and N below 2^30 (DG_ERR_UNSUPPORTED
+ * otherwise).  Returns a dg_status. */
 int dg_k_grouped_scatter_fp8(const void* x, const float* weights, const int32_t* slot_of, void* a, float* sfa, int T,
                              int top_k, int K, int N, int pow2_scales, void* stream);
 
@@ -379,14 +380,15 @@ int dg_k_grouped_scatter_fp8(const void* x, const float* weights, const int32_t*
  *   rows bf16 [M][N] (the masked form's [G][max_m][N] with M = G * max_m),
  *   row_of int32 [T][top_k], weights float [T][top_k] or NULL,
  *   c bf16 [T][N] or NULL (may equal d), d bf16 [T][N]
- * Any N; top_k at most 64 (DG_ERR_UNSUPPORTED otherwise).  Returns a dg_status. */
+ * N at most 2^30, odd ones too; top_k at most 64 (DG_ERR_UNSUPPORTED otherwise).
+ * Returns a dg_status. */
 int dg_m_grouped_gather(const void* rows, const int32_t* row_of, const float* weights, const void* c, void* d, int T,
                         int top_k, int M, int N, void* stream);
 
 /* Gradient of the gather with respect to its weights:
  *   grad_weights[t][j] = sum_n grad_d[t][n] * rows[row_of[t][j]][n]   (0 without a row)
  *   rows bf16 [M][N], grad_d bf16 [T][N], grad_weights float [T][top_k]
- * Returns a dg_status. */
+ * N at most 2^30, top_k at most 64.  Returns a dg_status. */
 int dg_m_grouped_gather_weight_grad(const void* rows, const int32_t* row_of, const void* grad_d, float* grad_weights,
                                     int T, int top_k, int M, int N, void* stream);
 
@@ -402,9 +404,9 @@ int dg_m_grouped_gather_weight_grad(const void* rows, const int32_t* row_of, con
  *   d  bf16 [T] rows of N values, ldd apart
  * A . x is summed, scaled and multiplied with B in fp32.  K must be a
  * multiple of 128, R a multiple of 8 and at most 256 (adapters of lower rank are
- * filled up with zeros); any N.  num_adapters at most 1024 (DG_ERR_UNSUPPORTED
- * otherwise).  Scratch: workspace (DG_ERR_UNSUPPORTED if a bound one has no room
- * for 16 tokens).  Returns a dg_status. */
+ * filled up with zeros), N at most 16776960, odd ones too, num_adapters at most
+ * 1024 (DG_ERR_UNSUPPORTED otherwise).  Scratch: workspace (DG_ERR_UNSUPPORTED if
+ * a bound one has no room for 16 tokens).  Returns a dg_status. */
 int dg_lora_bf16_nt(const void* x, int ldx, const void* a, const void* b, const float* scales,
                     const int32_t* adapter_ids, const void* c, int ldc, void* d, int ldd, int T, int N, int K, int R,
                     int num_adapters, void* stream);

@@ -848,6 +848,7 @@ extern "C" int dg_k_grouped_scatter_fp8(const void* x, const float* weights, con
   if (K < 0 || N < 0) return fail(DG_ERR_INVALID_ARG, "negative size (K=%d N=%d)", K, N);
   if (K % 128 != 0) return fail(DG_ERR_INVALID_ARG, "K=%d is not a multiple of 128", K);
   if (N % 16 != 0) return fail(DG_ERR_UNSUPPORTED, "the K-grouped product needs N a multiple of 16 (N=%d)", N);
+  if (N >= 1 << 30) return fail(DG_ERR_UNSUPPORTED, "N=%d must be below 2^30", N);     // 4 threads per column: a grid has 2^32
   if (K == 0 || N == 0) return DG_OK;
   if ((T > 0 && !x) || !slot_of || !a || !sfa)
     return fail(DG_ERR_INVALID_ARG, "x, slot_of, a and sfa must not be NULL");
