@@ -36,7 +36,7 @@ def section(name):
     at = header.index("int " + name + "(")
     text = header[header.rindex("/*", 0, at):at]
     general = header[header.index("The operators around the products ---"):]
-    return " ".join((general[:general.index("*/")] + text).replace(" * ", " ").split())
+    return " ".join((general[:general.index("*/")] + text).replace("\n * ", " ").split())
 
 
 @pytest.mark.parametrize("name,args,message,said", LIMITS, ids=[c[0] for c in LIMITS])
