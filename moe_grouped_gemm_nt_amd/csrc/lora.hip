@@ -583,6 +583,7 @@ int k_splits_for(bool listed, int tokens, long long tiles, int pieces, int num_c
   return (int)(n < 1 ? 1 : n);
 }
 
+constexpr int kTokensMost = 1 << 24;
 constexpr int kNoRoom = 1;               // not a dg_status: the scratch memory is too small for so many tokens
 
 int lora_tokens(LoraParams p, const Scratch& sc, hipStream_t st) {
@@ -690,8 +691,9 @@ extern "C" int dg_lora_bf16_nt(const void* x, int ldx, const void* a, const void
   p.K = K;
   p.R = R;
   p.L = terms ? num_adapters : 0;
-  // as many tokens at a time as the scratch memory has room for, usually all
-  int step = T;
+  // as many tokens at a time as the scratch memory has room for, usually all, and
+  // no more than a grid's threads (fewer than 2^32) and the lists' indices cover
+  int step = T < kTokensMost ? T : kTokensMost;
   for (int t = 0; t < T;) {
     const int n = T - t < step ? T - t : step;
     p.x = terms ? static_cast<const uint16_t*>(x) + (size_t)t * ldx : nullptr;
