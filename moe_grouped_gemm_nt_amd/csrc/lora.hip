@@ -294,8 +294,9 @@ __device__ __forceinline__ void sum_h(const LoraParams& p, const int* rows, int 
   }
 }
 
-// Eight neighbouring values of h as MFMA operands, v = part[0] + part[1] + part[2]
-// (an infinity or a NaN is part[0] alone).
+// Eight neighbouring values of h as MFMA operands, v = part[0] + part[1] + part[2]:
+// its leading eight bits, the next and the last (cut off, not rounded: the largest
+// values would round to infinity).  An infinity or a NaN is part[0] alone.
 constexpr int kParts = 3;
 __device__ __forceinline__ void split_h(const float* h, bf16x8 (&part)[kParts]) {
   const f32x4 h0 = *reinterpret_cast<const f32x4*>(h), h1 = *reinterpret_cast<const f32x4*>(h + 4);
@@ -304,9 +305,9 @@ __device__ __forceinline__ void split_h(const float* h, bf16x8 (&part)[kParts]) 
     float rest = e < 4 ? h0[e] : h1[e - 4];
 #pragma unroll
     for (int q = 0; q < kParts; ++q) {
-      part[q][e] = static_cast<__bf16>(rest);
-      const float back = static_cast<float>(part[q][e]);
-      rest = fabsf(back) < INFINITY ? rest - back : 0.0f;
+      const uint32_t head = __float_as_uint(rest) & 0xFFFF0000u;
+      part[q][e] = __builtin_bit_cast(__bf16, (uint16_t)(head >> 16));
+      rest = fabsf(rest) < INFINITY ? rest - __uint_as_float(head) : 0.0f;
     }
   }
 }

@@ -120,3 +120,26 @@ def test_the_inner_product_keeps_its_fp32_digits(dg, T, R):
     ref = ((x.double() @ a[0].double().t()) @ b[0].double().t()).numpy()
     assert np.abs(ref).max() > 0
     assert np.array_equal(d.float().cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_an_inner_product_at_the_end_of_fp32(dg, T):
+    # beyond bf16's largest value, 3.3895e38, and still an fp32 value; B brings it back
+    print(f"case: lora inner product of 3.4e38, {T} tokens", flush=True)
+    x = torch.zeros(T, 128, dtype=torch.bfloat16)
+    x[:, 0], x[:, 64] = 3.3895e38, 1e36
+    x[1], x[2] = -x[1], float("inf")
+    a = torch.ones(1, 8, 128, dtype=torch.bfloat16)
+    a[0, 1:] = 0.0
+    b = torch.zeros(1, 24, 8, dtype=torch.bfloat16)
+    b[0, :, 0] = 2.0 ** -100
+    d = torch.full((T, 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_lora_bf16_nt(x.cuda(), a.cuda(), b.cuda(), None, torch.zeros(T, dtype=torch.int32, device="cuda"), None, d)
+    torch.cuda.synchronize()
+    h = x[0].double().sum().item()
+    assert 3.397e38 < h < 3.4028e38
+    got = d.float().cpu()
+    want = torch.full((T, 24), h * 2.0 ** -100)
+    want[1] = -want[1]
+    keep = [t for t in range(T) if t != 2]                  # an infinity times ranks of 0 is a NaN
+    assert bool(((got - want).abs() <= 2.0 ** -8 * want.abs())[keep].all()) and bool(torch.isnan(got[2]).all())
