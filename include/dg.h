@@ -343,7 +343,10 @@ int dg_m_grouped_layout_masked(const int32_t* topk_ids, int T, int top_k, int fi
  *   v = weights[i] * x[t] (x[t] without weights),  sf = max(amax, 2^-100) / 448
  *   with amax = max |v| over the block (sf = 1 if amax = 0; with pow2_scales
  *   rounded up to a power of two),  a[r] = e4m3_rne(v / sf),
- * worked out to more than fp32 precision and rounded once, sf to fp32.
+ * worked out to more than fp32 precision; sf is then rounded to fp32 (an infinity
+ * beyond its range) and the quotient to fp32 and from there to e4m3, both to
+ * nearest even: a quotient within 2^-25 of itself of a value halfway between two
+ * codes counts as that value.
  *   x        bf16  [T][K] (16-byte aligned)
  *   weights  float [T][top_k] or NULL
  *   row_of, slot_of   the maps of the layout call; entries outside the range of

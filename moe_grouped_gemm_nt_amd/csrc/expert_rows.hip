@@ -253,11 +253,12 @@ typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ float bf16_f32(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 
-// Scales and codes are worked out in 64 bits and rounded once: a product of a
-// bf16 and an fp32 value is exact there, and blocks of bf16 values often hold
-// quotients that lie halfway between two codes, which fp32 roundings on the way
-// would tip to either side.  The fp64 units run at the fp32 rate here, and the
-// calls are bound by their bytes all the same.
+// Scales and quotients are worked out in 64 bits: a product of a bf16 and an fp32
+// value is exact there, and blocks of bf16 values often hold quotients that lie
+// halfway between two codes, which fp32 roundings on the way would tip to either
+// side.  The quotient is rounded to fp32 at the end, which takes the last fp64
+// roundings out of such ties again, and then to a code.  The fp64 units run at the
+// fp32 rate here, and the calls are bound by their bytes all the same.
 
 // The scale of a block whose largest magnitude is amax (include/dg.h).
 __device__ __forceinline__ float scale_of(double amax, bool pow2) {
@@ -330,8 +331,8 @@ constexpr int SJ = 8;                    // rows a thread writes per turn; also 
 // with them the products are quantised per row).  In each group of eight lanes,
 // lane i also works out and stores the scale of row i of the turn.  Bound by the
 // bytes: 65536 rows of 7168 from 8192 tokens take 118 us without their scales
-// (4.97 TB/s), 8192 rows from 4096 tokens 26.5 us with them (4.5 TB/s); one
-// workgroup per row, reading its token again for each, took 255 and 34.
+// (4.97 TB/s; with weights 120), 8192 rows from 4096 tokens 26.5 us with them (4.5
+// TB/s); one workgroup per row, reading its token again for each, took 255 and 34.
 template <bool WEIGHTED, bool MASKED, bool TABLE>
 __global__ __launch_bounds__(256) void scatter_kernel(ScatterParams p, float* table, int ld) {
   const int per_token = p.K / 16;
@@ -426,8 +427,9 @@ struct KScatterParams {
 // remainder by FMA); the weighted maxima take fp64 instructions, and so do the
 // codes of a block where a product is beyond fp32's range.  A row is read
 // and written once; bound by the chain of map, row and maxima before the first
-// store: 9088 rows of 4096 columns, weighted, take 23.6 us (3.05 TB/s) in
-// workgroups of 512 threads, 24.9 in ones of 256 with 8 rows per thread.
+// store: 9088 rows of 4096 columns take 23.7 us weighted (3.05 TB/s) and 18.9
+// unweighted in workgroups of 512 threads, 24.9 weighted in ones of 256 with 8 rows
+// per thread.
 constexpr int KT = 512;                  // threads per workgroup
 constexpr int KR = 128 * 16 / KT;        // rows per thread
 constexpr int kMaxGridY = 65535;         // a grid's second axis; what is beyond goes on the third
@@ -695,9 +697,13 @@ int launched() {
 
 // ---- argument checks shared by the entry points ------------------------------
 constexpr long long kMaxChoices = 1LL << 30;
-// Scales row by row from here on: at 65536 rows of 7168 the two kernels take 129 us
-// against 142 in one; at 8192 rows the scales' scattered words cost 1.5 us of 27,
-// less than a second launch.
+// Scales row by row from here on, by the rows that there are: with 65536 of 98048
+// rows of 7168 in use the two kernels take 130 us against 142 in one, with 32768 of
+// 65280 56 against 75, with 16384 of 48896 29 against 31, with 8192 of 40704 the
+// same.  Below 32768 rows few can be in use (8192: the scales' scattered words cost
+// 1.5 us of 27, less than a second launch).  Buffers of more rows that are nearly
+// empty pay for the second launch: 512 choices in 256 x 128 masked rows take 7.0
+// us against 4.4.
 constexpr long long kScaleRows = 32768;
 constexpr long long kMaxGrid = 1 << 23;  // workgroups: a grid's thread count has 32 bits
 

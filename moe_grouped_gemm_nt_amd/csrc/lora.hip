@@ -13,8 +13,8 @@ constexpr int THREADS = 256;
 constexpr int WAVES = THREADS / 64;
 // Up to here every workgroup finds its tile's tokens itself; beyond, layout kernels
 // make lists.  Measured beside a 2112 x 7168 projection at 256 tokens against 257:
-// one adapter of rank 16 14.5 us against 16.8, 48 of them 14.9 against 18.5, 8 of
-// rank 64 22.9 against 21.1; at 128 tokens 10.0, 11.0 and 14.4 us.
+// one adapter of rank 16 15.2 us against 17.2, 48 of them 15.4 against 18.4, 8 of
+// rank 64 23.2 against 23.0; at 128 tokens 10.4, 11.4 and 15.8 us.
 constexpr int kInlineTokens = 256;
 
 struct LoraParams {
@@ -124,7 +124,7 @@ __device__ __forceinline__ bf16x8 piece_operand(const uint8_t* rows, int row, in
 
 // Many tokens: 64 to a tile, 16 to a wave; the waves load each piece together
 // into a ring of slots, RING - 1 of them ahead of the products.  8192 tokens of
-// 7168 with 8 adapters of rank 64: 33 us, 3.6 TB/s of x.
+// 7168 with 8 adapters of rank 64: 34 us, 3.4 TB/s of x.
 template <int RT>
 __global__ __launch_bounds__(THREADS) void lora_shrink_listed_kernel(LoraParams p) {
   constexpr int BT = kTile<true>;
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(THREADS) void lora_shrink_listed_kernel(LoraParams 
 
 // Few tokens: a tile of 16, whose pieces the four waves take in turn, each with
 // LDS of its own (no barrier), UP pieces at a time and all of them in flight.  64
-// tokens of 48 adapters of rank 16, K 7168: 5.1 us (11 MB of A and x), of which a
+// tokens of 48 adapters of rank 16, K 7168: 5.3 us (11 MB of A and x), of which a
 // launch is about 2.3; the rest is the chain of ids, lines and sums.
 template <int RT>
 __global__ __launch_bounds__(THREADS) void lora_shrink_few_kernel(LoraParams p) {
@@ -313,7 +313,7 @@ __device__ __forceinline__ void split_h(const float* h, bf16x8 (&part)[kParts]) 
 }
 
 // Few tokens: a tile of 16, the waves side by side on 16 * NT columns each (the
-// same call's 2112 columns: 5.2 us, latency).
+// same call's 2112 columns: 5.7 us at NT = 1, latency).
 // MFMA row r of sub-tile j stands for column 4 * NT * (r / 4) + 4 * j + r % 4, so
 // that a lane's 4 * NT results are neighbours in d.
 template <int RK, int NT>
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(THREADS) void lora_expand_few_kernel(LoraParams p) 
 // of a step are contiguous and come into LDS for the four waves with direct
 // loads, a step ahead; results pass through LDS so that c and d are read and
 // written in whole 128-byte lines (8 rows of 64 columns per instruction).  Bound
-// by c and d: 8192 tokens, 4096 columns, rank 64 take 38 us (3.5 TB/s of c and d),
+// by c and d: 8192 tokens, 4096 columns, rank 64 take 39 us (3.5 TB/s of c and d),
 // 5 of them for the partial sums; with operands and results straight from and to
 // memory, in 64-byte pieces of sixteen rows, it took 78.
 template <int RK>
@@ -559,9 +559,10 @@ void launch_expand_few(LoraParams p, hipStream_t st) {
 template <int RK, int SLOTS>
 void launch_expand_listed(LoraParams p, int num_cus, hipStream_t st) {
   const int chunks = (p.N + 63) / 64;
-  // as many workgroups as run at once (SLOTS per CU, by their LDS), so that no CU
-  // has a last one to itself (8192 tokens, rank 64, 4096 columns: 38 us against 40
-  // with two per CU and a few more); a workgroup's steps share one sum of h
+  // as many workgroups as run at once (SLOTS per CU: what their LDS has room for,
+  // and no more than four), so that no CU has a last one to itself (8192 tokens, rank
+  // 64, 4096 columns, the whole call: 73 us against 78 with two per CU and a few
+  // more); a workgroup's steps share one sum of h
   long long parts = (long long)SLOTS * num_cus / p.tiles;
   parts = parts < 1 ? 1 : (parts > chunks ? chunks : parts);
   p.steps = (int)((chunks + parts - 1) / parts);
@@ -570,12 +571,15 @@ void launch_expand_listed(LoraParams p, int num_cus, hipStream_t st) {
   lora_expand_listed_kernel<RK><<<grid, THREADS, 0, st>>>(p);
 }
 
-// K ranges: as many workgroups as run at once (three per CU with lists, by their
-// LDS; a further round for a few of them would cost as much as the others
-// together), and at least a piece for each of the four waves.
+// K ranges: three workgroups per CU with lists, as many as run at once at ranks 33
+// to 64 (a further round for a few of them would cost as much as the others
+// together), and two without; and at least a piece for each of the four waves.  The
+// same at every rank, although the LDS has room for 5, 4, 3, 2 and 1 with lists up
+// to ranks 16, 32, 64, 128 and 256, and for 2, 3, 1, 2 and 1 without: the other
+// ranks' own numbers are not measured.
 // Without lists every token has a workgroup per range, most of which may find that
 // they have no tile: no more than four of those per CU (128 tokens of 8 adapters of
-// rank 64: 14.4 us against 23.9 without this limit).
+// rank 64: 15.8 us against 23.5 without this limit).
 int k_splits_for(bool listed, int tokens, long long tiles, int pieces, int num_cus) {
   long long fit = (listed ? 3LL : 2LL) * num_cus / tiles;
   if (!listed && fit > 4LL * num_cus / tokens) fit = 4LL * num_cus / tokens;
@@ -639,8 +643,8 @@ int lora_tokens(LoraParams p, const Scratch& sc, hipStream_t st) {
   } else {
     if (terms) launch_shrink<false>(p, st);
     // 64 columns per wave where that makes four workgroups per CU, 16 below (2112
-    // columns, 8 adapters of rank 64: 64 tokens 10.6 us against 9.6, 128 tokens 14.5
-    // against 15.6; 48 of rank 16: 9.2 against 9.0 and 11.1 against 12.5)
+    // columns, 8 adapters of rank 64: 64 tokens 13.3 us against 12.1, 128 tokens 15.8
+    // against 15.9; 48 of rank 16: 9.9 against 9.8 and 11.4 against 13.3)
     if (tiles * ((p.N + 255) / 256) >= 4 * sc.num_cus)
       launch_expand_few<4>(p, st);
     else

@@ -469,9 +469,11 @@ __device__ __forceinline__ void softmax16(const float (&x)[NI], float (&y)[NI], 
 // size is a multiple of 4 here).  Each lane sorts its own keys down to the D
 // highest; a choice is then the highest head of the sixteen lists, four DPP
 // steps, and its owner's list moves up.  Bound by the VALU at many tokens (16384
-// tokens, 256 experts in 8 groups, 8 choices: 9.9 us, 1.8 TB/s, where one wave per
-// token that searches all its keys for every choice takes 44) and by the chain of
-// dependent instructions at few (64 tokens: 5.1 us against 11.9).
+// tokens, 256 experts in 8 groups, 8 choices: 11.3 us, 1.5 TB/s; 1265 VALU
+// instructions per wave fill four fifths of the SIMDs' cycles; one wave per token
+// that searches all its keys for every choice took 44) and by the chain of loads
+// and dependent instructions at few (64 tokens: 5.8 us, a third of it VALU issue;
+// one wave per token took 11.9).
 template <int NI, int D, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(256) void route16_kernel(RouteParams p) {
   constexpr int Q = NI / 4;
@@ -583,8 +585,8 @@ __global__ __launch_bounds__(256) void route16_kernel(RouteParams p) {
 
 // The gradient, sixteen lanes per token (formulas at route_backward_kernel): lane j
 // on the j-th choice, whose term reaches the expert's lane through LDS.  Softmax
-// over 60 bf16 logits of 20479 tokens: 4.5 us, of which the bytes need 1.1 and a
-// launch about 2; one wave per token takes 9.8.
+// over 60 bf16 logits of 20479 tokens: 4.4 us, of which the bytes need 1.1 and a
+// launch about 2; one wave per token took 9.8.
 template <int NI, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(256) void route16_backward_kernel(RouteParams p) {
   __shared__ f32x4 lds_u[16][NI * 4];          // [token of the workgroup][quad of experts]
