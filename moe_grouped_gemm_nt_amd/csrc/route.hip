@@ -86,6 +86,19 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// The sum of the other lanes' values, added up as such: not a total less this
+// lane's value, which has no digits left where that is nearly all of it.
+__device__ __forceinline__ float wave_others(float v) {
+  float others = 0.0f;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float w = __shfl_xor(v, o);
+    others += w;
+    v += w;
+  }
+  return others;
+}
+
 // The sum of a group's two highest keys: as an fp32 sum, but without its range, so
 // that two keys of the lowest finite value still have a score (-inf would mask the
 // group) and two of the highest do not tie with +inf.
@@ -209,11 +222,24 @@ __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteParams p) {
   }
 }
 
-// Gradient: with w_j = scale * s_j (/ sum of the chosen s) and u_j = g_j * w_j,
-//   renormalised:  u_j -= (w_j / scale) * sum_i u_i
-//   sigmoid:       dx_j = u_j * sigmoid(-x_j), 0 elsewhere   (d log sigmoid(x) = 1 - sigmoid(x),
-//                  which as a difference would have no digits left for large x)
-//   softmax:       dx_i = [i chosen] u_i - p_i * sum_j u_j   (the sum is 0 when renormalised)
+// Gradient: with the chosen scores' shares r_j = s_j (/ sum of the chosen s) and g_j
+// the weights' gradients times scale,
+//   renormalised:  u_j = r_j (g_j sum_{i != j} r_i - sum_{i != j} r_i g_i)
+//   otherwise:     u_j = s_j g_j
+//   sigmoid:       dx_j = u_j * sigmoid(-x_j), 0 elsewhere   (d log sigmoid(x) = 1 - sigmoid(x))
+//   softmax:       renormalised dx_j = u_j, 0 elsewhere; otherwise, p the softmax,
+//                  dx_j = p_j (g_j (1 - p_j) - sum_{i != j} p_i g_i) for the chosen,
+//                  dx_e = -p_e sum_i p_i g_i elsewhere
+// What a share leaves is summed from the others' (1 - p_j from p_j = 3/4 on, from
+// the p up to 1/2), not subtracted from 1: where one choice takes nearly all, a
+// difference has no digits left.
+// The experts without a term of their own bear this mark, a NaN (a term that is the
+// same NaN makes the sum, and so what stands for the mark, a NaN too).
+constexpr uint32_t kNotChosen = 0x7FFFFFFF;
+__device__ __forceinline__ float softmax_term(float s, float g, float rest, float others) {
+  const float less = s > 0.75f ? rest : 1.0f - s;
+  return s > 0.0f ? s * (g * less - others) : 0.0f;
+}
 // One wave per token, lane j on the j-th choice; the chosen terms go through LDS.
 template <int NI, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams p) {
@@ -222,6 +248,7 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
   const unsigned t = blockIdx.x * WAVES + wave;
   const bool live = t < (unsigned)p.T;
   const size_t row = (size_t)(live ? t : 0) * p.E;
+  const bool spread = !SIGMOID && !p.renormalize;        // every expert has a gradient
   float x[NI];
   float top = -INFINITY;
 #pragma unroll
@@ -229,7 +256,7 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
     const int e = lane + 64 * i;
     x[i] = e < p.E ? clean_logit(raw_logit<BF16>(p.logits, row + e)) : -INFINITY;
     top = fmaxf(top, x[i]);
-    lds_u[wave][lane + 64 * i] = 0.0f;
+    lds_u[wave][lane + 64 * i] = spread ? __uint_as_float(kNotChosen) : 0.0f;
   }
   float inv = 0.0f;
   if constexpr (!SIGMOID) {
@@ -256,25 +283,30 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(RouteParams 
       }
     }
   }
-  float share = s;                                // w_j / scale
+  float u = s > 0.0f ? g * s : 0.0f, sum = 0.0f;
   if (p.renormalize) {
     const float total = wave_sum(s);
-    share = total > 0.0f ? s / total : 0.0f;
+    const float share = total > 0.0f ? s / total : 0.0f;
+    const float less = wave_others(share), others = wave_others(s > 0.0f ? g * share : 0.0f);
+    u = s > 0.0f ? share * (g * less - others) : 0.0f;
+  } else if (spread) {
+    float rest = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) rest += x[i] * inv <= 0.5f ? x[i] * inv : 0.0f;
+    rest = wave_sum(rest);
+    sum = wave_sum(u);
+    u = softmax_term(s, g, rest, wave_others(u));
   }
-  float u = s > 0.0f ? g * share : 0.0f;
-  const float sum = wave_sum(u);
-  if (p.renormalize) u -= share * sum;
   __syncthreads();
   if (id >= 0) lds_u[wave][id] = SIGMOID ? u * sigmoid_any(-xi) : u;
   __syncthreads();
   if (!live) return;
-  const float back = !SIGMOID && !p.renormalize ? sum : 0.0f;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int e = lane + 64 * i;
     if (e >= p.E) continue;
     float d = lds_u[wave][e];
-    if constexpr (!SIGMOID) d -= x[i] * inv * back;
+    if constexpr (!SIGMOID) d = spread && __float_as_uint(d) == kNotChosen ? fmaf(-x[i] * inv, sum, 0.0f) : d;
     if constexpr (BF16)
       static_cast<__bf16*>(p.grad_logits)[row + e] = static_cast<__bf16>(d);
     else
@@ -347,6 +379,18 @@ __device__ __forceinline__ float row_sum(float v) {
   v += dpp<kXor2>(v);
   v += dpp<kHalfMirror>(v);
   return v + dpp<kMirror>(v);
+}
+
+__device__ __forceinline__ float row_others(float v) {             // as wave_others, of sixteen lanes
+  float w = dpp<kXor1>(v), others = w;
+  v += w;
+  w = dpp<kXor2>(v);
+  others += w;
+  v += w;
+  w = dpp<kHalfMirror>(v);
+  others += w;
+  v += w;
+  return others + dpp<kMirror>(v);
 }
 
 __device__ __forceinline__ void order(double& a, double& b) {     // a >= b afterwards
@@ -585,7 +629,7 @@ __global__ __launch_bounds__(256) void route16_kernel(RouteParams p) {
 
 // The gradient, sixteen lanes per token (formulas at route_backward_kernel): lane j
 // on the j-th choice, whose term reaches the expert's lane through LDS.  Softmax
-// over 60 bf16 logits of 20479 tokens: 4.4 us, of which the bytes need 1.1 and a
+// over 60 bf16 logits of 20479 tokens: 4.5 us, of which the bytes need 1.1 and a
 // launch about 2; one wave per token took 9.8.
 template <int NI, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(256) void route16_backward_kernel(RouteParams p) {
@@ -594,8 +638,10 @@ __global__ __launch_bounds__(256) void route16_backward_kernel(RouteParams p) {
   const size_t t = (size_t)blockIdx.x * 16 + local;
   const bool live = t < (size_t)p.T;
   const size_t row = (live ? t : (size_t)p.T - 1) * p.E;
+  const bool spread = !SIGMOID && !p.renormalize;        // every expert has a gradient
+  const float blank = spread ? __uint_as_float(kNotChosen) : 0.0f;
 #pragma unroll
-  for (int q = 0; q < NI / 4; ++q) lds_u[local][q * 16 + lane] = f32x4{};
+  for (int q = 0; q < NI / 4; ++q) lds_u[local][q * 16 + lane] = f32x4{blank, blank, blank, blank};
   int id = -1;
   float g = 0.0f, xi = -INFINITY;
   if (live && lane < p.top_k) {
@@ -614,20 +660,25 @@ __global__ __launch_bounds__(256) void route16_backward_kernel(RouteParams p) {
     softmax16(x, y, top, inv);
   }
   const float s = xi > -INFINITY ? (SIGMOID ? sigmoid_any(xi) : exp_any(xi - top) * inv) : 0.0f;
-  float share = s;                             // w_j / scale
+  float u = s > 0.0f ? g * s : 0.0f, sum = 0.0f;
   if (p.renormalize) {
     const float total = row_sum(s);
-    share = total > 0.0f ? s / total : 0.0f;
+    const float share = total > 0.0f ? s / total : 0.0f;
+    const float less = row_others(share), others = row_others(s > 0.0f ? g * share : 0.0f);
+    u = s > 0.0f ? share * (g * less - others) : 0.0f;
+  } else if constexpr (!SIGMOID) {
+    float rest = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) rest += y[i] <= 0.5f ? y[i] : 0.0f;
+    rest = row_sum(rest);
+    sum = row_sum(u);
+    u = softmax_term(s, g, rest, row_others(u));
   }
-  float u = s > 0.0f ? g * share : 0.0f;
-  const float sum = row_sum(u);
-  if (p.renormalize) u -= share * sum;
   // one wave writes and reads a token's words: program order is enough
   __builtin_amdgcn_wave_barrier();
   if (id >= 0) reinterpret_cast<float*>(&lds_u[local][0])[id] = SIGMOID ? u * sigmoid_any(-xi) : u;
   __builtin_amdgcn_wave_barrier();
   if (!live) return;
-  const float back = !SIGMOID && !p.renormalize ? sum : 0.0f;
 #pragma unroll
   for (int q = 0; q < NI / 4; ++q) {
     const int e = q * 64 + lane * 4;
@@ -635,7 +686,8 @@ __global__ __launch_bounds__(256) void route16_backward_kernel(RouteParams p) {
     f32x4 d = lds_u[local][q * 16 + lane];
     if constexpr (!SIGMOID)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] -= y[4 * q + i] * back;
+      for (int i = 0; i < 4; ++i)
+        d[i] = spread && __float_as_uint(d[i]) == kNotChosen ? fmaf(-y[4 * q + i], sum, 0.0f) : d[i];
     if constexpr (BF16) {
       u16x4 h;
 #pragma unroll

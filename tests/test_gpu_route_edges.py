@@ -150,3 +150,71 @@ def test_group_scores_beyond_the_finite_range(dg, E, G):
         ids, _, _ = around.route(x, bias, 1, "sigmoid", G, 1, 2)
         got_ids, _ = run(dg, x, bias, 1, score="sigmoid", num_groups=G, topk_groups=1, group_top=2)
         assert np.array_equal(got_ids, ids), at
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(2, 1)] + PATHS)
+def test_gradient_of_a_choice_that_takes_nearly_all(dg, E, k, score, renorm):
+    # one expert's share is 1 - e^-5 to 1 - e^-38: its gradient is its share times what the others have
+    print(f"case: gradient of a dominant choice {score} E={E} top_k={k} renormalize={renorm}", flush=True)
+    rng = np.random.default_rng(E * 7 + k)
+    T, scale = 34, 1.5
+    x = rng.standard_normal((T, E)).astype(np.float32) - (40.0 if score == "sigmoid" else 0.0)
+    x[np.arange(T), rng.integers(0, E, T)] += np.linspace(5.0, 38.0, T).astype(np.float32)
+    x[5, 0] = x[5, 1] = x[5].max()                       # two of the highest
+    x[7, x[7] < x[7].max()] = -np.inf                    # nothing beside it
+    ids, _, _ = around.route(x, None, k, score)
+    g = rng.standard_normal((T, k)).astype(np.float32)
+    got = backward(dg, x, ids, g, score=score, renormalize=renorm, scale=scale)
+    xd = x.astype(np.float64)
+    p = 1.0 / (1.0 + np.exp(-xd)) if score == "sigmoid" else np.exp(xd - xd.max(axis=1, keepdims=True))
+    if score == "softmax":
+        p /= p.sum(axis=1, keepdims=True)
+    want, size = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        i = ids[t][ids[t] >= 0]
+        gt, pt = g[t, :i.size].astype(np.float64), p[t, i]
+        if renorm:
+            pt = pt / pt.sum()
+        for j in range(i.size):
+            rest = np.arange(i.size) != j
+            if renorm:                                   # sums of what is not j, never 1 - share
+                less = pt[rest].sum()
+            elif score == "softmax":
+                less = np.delete(p[t], i[j]).sum()
+            else:
+                less = 1.0
+            others = pt[rest] if renorm or score == "softmax" else 0.0 * pt[rest]
+            own = 1.0 / (1.0 + np.exp(xd[t, i[j]])) if score == "sigmoid" else 1.0
+            want[t, i[j]] = scale * own * pt[j] * (gt[j] * less - (others * gt[rest]).sum())
+            size[t, i[j]] = scale * own * pt[j] * (abs(gt[j]) * less + (others * np.abs(gt[rest])).sum())
+        if score == "softmax" and not renorm:
+            free = np.setdiff1d(np.arange(E), i)
+            want[t, free] = -scale * p[t, free] * (pt * gt).sum()
+            size[t, free] = scale * p[t, free] * (pt * np.abs(gt)).sum()
+    # x - top rounds to 2^-24 of at most 45, 3e-6 in each of a product's two shares; the rest as above.
+    # Subnormal scores stand a unit of 2^-149 apart
+    assert np.all(np.abs(got - want) <= 2e-5 * size + 4.0 * LEAST)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", PATHS)
+def test_a_nan_gradient_stays_one(dg, E, k, score, renorm):
+    # whichever bits it has; and a token of masked experts only has none
+    print(f"case: route gradient of NaN {score} E={E} top_k={k} renormalize={renorm}", flush=True)
+    rng = np.random.default_rng(E)
+    x = rng.standard_normal((6, E)).astype(np.float32)
+    x[5] = -np.inf
+    x[4, ::2] = -np.inf
+    ids, _, _ = around.route(x, None, k, score)
+    g = rng.standard_normal((6, k)).astype(np.float32)
+    bits = g.view(np.uint32)
+    bits[0, 1], bits[1, 0], bits[2, 2], bits[5] = 0x7FFFFFFF, 0x7FC00000, 0xFFFFFFFF, 0x7FFFFFFF
+    got = backward(dg, x, ids, g, score=score, renormalize=renorm, scale=1.0)
+    for t, j in ((0, 1), (1, 0), (2, 2)):
+        assert np.isnan(got[t, ids[t, j]])
+        if score == "softmax" and not renorm:
+            assert np.isnan(got[t]).all()
+    assert np.isfinite(got[3:]).all() and np.all(got[5] == 0.0) and np.all(got[4, ::2] == 0.0)
