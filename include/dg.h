@@ -220,7 +220,9 @@ int dg_choose_config(int form, int rows, int N, int K, int num_groups, int num_c
  * every later call of this library enqueued on that stream uses it in place of
  * the device's shared workspace (split-K partial tiles and scale-check
  * verdicts; and what the operators around the products put there: the layouts'
- * counts, the scatters' block maxima, the adapters' lists and partial sums), so
+ * counts, the scatters' block maxima, the adapters' lists and partial sums, the
+ * lists of the 4-bit products by choice, the balance loss's and the norm's partial
+ * sums), so
  * that calls running at the same time on different streams no longer share
  * scratch memory. workspace: device memory on the current device, 256-byte
  * aligned, at least 256 bytes (the verdicts). A workspace of at least 256 +
@@ -258,7 +260,9 @@ int dg_check_grouped_layout(const int32_t* grouped_layout, int M, int num_groups
  * row of the M-grouped (or K-grouped) products, the scatter calls move and
  * quantise the tokens' rows there, the gather call sums the experts' results
  * back per token, and the adapter call adds low-rank terms to (or ahead of) a
- * dense projection.  They follow the rules above: device pointers owned by the
+ * dense projection.  Beside them stand the router's balance loss, products of a
+ * few tokens with 4-bit weights, and the norm and clipping of the gradients.  They
+ * follow the rules above: device pointers owned by the
  * caller, checks on the host, no synchronisation, capturable in a HIP graph
  * after dg_init(), and the device's (or the stream's bound) workspace as
  * scratch where a call says so.  An array of no elements may be NULL.  T * top_k
@@ -413,6 +417,121 @@ int dg_m_grouped_gather_weight_grad(const void* rows, const int32_t* row_of, con
 int dg_lora_bf16_nt(const void* x, int ldx, const void* a, const void* b, const float* scales,
                     const int32_t* adapter_ids, const void* c, int ldc, void* d, int ldd, int T, int N, int K, int R,
                     int num_adapters, void* stream);
+
+/* The router's balance loss and the experts' counts.  The tokens are num_seqs
+ * sequences, one behind the other: sequence s has the n_s tokens from
+ * seq_starts[s] to seq_starts[s+1] - 1, and with p[t] = softmax(logits[t]) or
+ * sigmoid(logits[t]) divided by the sum of the token's sigmoids
+ *   counts[s][e] = choices of e among the sequence's topk_ids
+ *   loss[s] = scale * E / (top_k * n_s^2) * sum_e counts[s][e] * sum_{t in s} p[t][e]
+ * which is scale where every expert has the same share (0 for a sequence of no
+ * tokens).
+ *   logits  logits_type [T][E]; topk_ids int32 [T][top_k], ids outside [0, E) are
+ *           not counted
+ *   seq_starts int32 [num_seqs + 1], rising (not necessarily strictly), or NULL
+ *           with num_seqs 1: all tokens.  Tokens before seq_starts[0] and from
+ *           seq_starts[num_seqs] on (padding) take no part.  Entries outside
+ *           [0, T] count as 0 or T
+ *   loss float [num_seqs], counts int32 [num_seqs][E]   outputs
+ * A logit of -inf or NaN is a masked expert's: its share is 0.  A token of masked
+ * experts only has no shares, but counts in n_s.  +inf counts as the largest
+ * finite value.  Sigmoids keep their shares however far below zero all of a
+ * token's logits lie; shares below 2^-126 are 0.  E at most 1024, top_k at most
+ * 64, T * top_k at most 2^30 (DG_ERR_UNSUPPORTED otherwise).  Scratch: workspace
+ * (DG_ERR_UNSUPPORTED if a bound one has no room for 16 bytes per expert, E
+ * rounded up to a multiple of 4).  Returns a dg_status. */
+int dg_route_balance(const void* logits, int logits_type, const int32_t* topk_ids, const int32_t* seq_starts,
+                     float* loss, int32_t* counts, int T, int E, int top_k, int num_seqs, int score, float scale,
+                     void* stream);
+
+/* Gradient of the balance loss with respect to the logits, for the forward call's
+ * counts (constants: a choice has no gradient):
+ *   grad_logits[t][i] = c[t][i] + grad_loss[s] * d loss[s] / d logits[t][i]
+ *   logits, c, grad_logits  logits_type [T][E]; c NULL means 0 and may equal
+ *           grad_logits: the gradient of the routing weights, to which this is added
+ *   grad_loss float [num_seqs] or NULL (ones); counts, seq_starts as above
+ * A masked expert and a token of no sequence get c.  One rounding to logits_type.
+ * Returns a dg_status. */
+int dg_route_balance_backward(const void* logits, int logits_type, const int32_t* counts, const int32_t* seq_starts,
+                              const float* grad_loss, const void* c, void* grad_logits, int T, int E, int top_k,
+                              int num_seqs, int score, float scale, void* stream);
+
+/* Products of a few tokens with 4-bit weights and unquantised activations:
+ *   d[m][n] = bf16_rne( c[m][n] + sum_k x[m][k] * w[n][k] )
+ * for the tokens of a decoding step, where reading the weights is all the time.
+ * The FP4 form takes the weights of dg_fp8_fp4_gemm_nt as they are stored:
+ *   w[n][k] = e2m1(b[n][k]) * 2^(e[n][k/32] - 127), as a bf16 value: exact, but
+ *           rounded to it below 2^-126, and an infinity from 2^128 on; a NaN
+ *           where e = 255
+ *   b uint8 [N][K/2] (16-byte aligned), sfb int32 [K/128][N] (4-byte aligned)
+ * the integer form groups of group_size (32, 64 or 128) values along K:
+ *   w[n][k] = (q[n][k] - zeros[k/group_size][n]) * scales[k/group_size][n]
+ *   b uint8 [N][K/2], two q of 0 to 15 per byte, element 2i in the low nibble
+ *           (16-byte aligned)
+ *   scales scales_type [K/group_size][N]  DG_F32 or DG_BF16
+ *   zeros uint8 [K/group_size][N] or NULL: 8
+ * A group's sum of x * q and its sum of x are fp32 sums, joined and scaled in fp32.
+ *   x  bf16 [M] rows of K values, ldx apart (16-byte aligned, ldx % 8 == 0)
+ *   c  bf16 [M] rows of N values, ldc apart, or NULL (0); may equal d
+ *   d  bf16 [M] rows of N values, ldd apart
+ * x is finite in the integer form (an infinity makes its token's results NaN).  K
+ * must be a multiple of 128, N at most 2^20, odd ones too (DG_ERR_UNSUPPORTED
+ * otherwise).  Any M, in tiles of 16 tokens that each read the weights: from a few
+ * hundred tokens on the FP8 products take less time.  Returns a dg_status. */
+int dg_bf16_fp4_gemv_nt(const void* x, int ldx, const void* b, const int32_t* sfb, const void* c, int ldc, void* d,
+                        int ldd, int M, int N, int K, void* stream);
+int dg_bf16_int4_gemv_nt(const void* x, int ldx, const void* b, const void* scales, int scales_type, const void* zeros,
+                         int group_size, const void* c, int ldc, void* d, int ldd, int M, int N, int K, void* stream);
+
+/* The same with the experts of every choice, straight from the router's ids: no
+ * layout, no rows moved, an expert's weights read once for its choices (16 at a
+ * time).  Choice i = t * top_k + j of expert e = topk_ids[t][j], local expert
+ * g = e - first_expert in [0, num_groups):
+ *   d[i][n] = bf16_rne( c[i][n] + sum_k x[row][k] * w[g][n][k] )
+ *   x  rows of K values as above: x_rows = T, a token's choices sharing row t, or
+ *      x_rows = T * top_k, row i each (the experts' way back down)
+ *   b, sfb, scales, zeros  as above with a leading axis [num_groups]
+ *   c, d  rows of N values for T * top_k choices, as above
+ * A choice whose expert is not here gets c (zeros without one), so that a gather
+ * with row_of[t][j] = t * top_k + j sums what this GPU's experts give.  num_groups
+ * at most 1024, T * top_k at most 2^30.  Scratch: workspace (lists, from 513
+ * choices on; a small one costs speed only).  Returns a dg_status. */
+int dg_m_grouped_bf16_fp4_gemv_nt_topk(const void* x, int ldx, int x_rows, const int32_t* topk_ids, const void* b,
+                                       const int32_t* sfb, const void* c, int ldc, void* d, int ldd, int T, int top_k,
+                                       int first_expert, int num_groups, int N, int K, void* stream);
+int dg_m_grouped_bf16_int4_gemv_nt_topk(const void* x, int ldx, int x_rows, const int32_t* topk_ids, const void* b,
+                                        const void* scales, int scales_type, const void* zeros, int group_size,
+                                        const void* c, int ldc, void* d, int ldd, int T, int top_k, int first_expert,
+                                        int num_groups, int N, int K, void* stream);
+
+/* The norm of all gradients together, such as the K-grouped product's and the
+ * others of a training step:
+ *   norm[0] = sqrt( sum over all tensors and elements of grads[i][j]^2 )
+ * Squares and sums are fp64; the result is rounded to fp32.
+ *   grads  num_tensors addresses, types their dg_dtypes, sizes their elements:
+ *          arrays on the HOST, read during the call (they travel in the launches'
+ *          arguments: a captured graph replays with the tensors of the captured
+ *          call).  Each tensor is contiguous and aligned to its type; one of size
+ *          0 may be NULL
+ *   norm float [1]   output
+ * No tensors have a norm of 0.  num_tensors at most 2^20, a tensor at most 2^43
+ * elements (DG_ERR_UNSUPPORTED otherwise).  Scratch: workspace (8 bytes per 120
+ * tensors at the least, DG_ERR_UNSUPPORTED if a bound one has less).  Returns a
+ * dg_status. */
+int dg_grad_norm(const void* const* grads, const int* types, const long long* sizes, int num_tensors, float* norm,
+                 void* stream);
+
+/* The gradients scaled so that their norm is at most max_norm:
+ *   out[i][j] = grads[i][j] * f,   f = min(1, max_norm / (norm[0] + 1e-6))
+ * f in fp32, one rounding to each tensor's type.  norm is read by the kernels only,
+ * so that a job may sum the squares of several GPUs in between.  A NaN norm makes f
+ * NaN, an infinite one 0.
+ *   grads, types, sizes as above; out num_tensors addresses on the HOST: each may
+ *   equal grads[i], and otherwise shares no memory with any tensor or with norm
+ *   (DG_ERR_INVALID_ARG otherwise).  max_norm must not be negative.
+ * Returns a dg_status. */
+int dg_grad_clip(const void* const* grads, void* const* out, const int* types, const long long* sizes,
+                 int num_tensors, const float* norm, float max_norm, void* stream);
 
 /* Prepares per-device state for the current HIP device (device properties and
  * the split-K workspace, allocated once and kept until the process ends).

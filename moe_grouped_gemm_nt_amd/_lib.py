@@ -42,6 +42,14 @@ EXPORTED = [
     "dg_m_grouped_gather",
     "dg_m_grouped_gather_weight_grad",
     "dg_lora_bf16_nt",
+    "dg_route_balance",
+    "dg_route_balance_backward",
+    "dg_bf16_fp4_gemv_nt",
+    "dg_bf16_int4_gemv_nt",
+    "dg_m_grouped_bf16_fp4_gemv_nt_topk",
+    "dg_m_grouped_bf16_int4_gemv_nt_topk",
+    "dg_grad_norm",
+    "dg_grad_clip",
     "dg_choose_config",
     "dg_check_grouped_layout",
     "dg_bind_stream_workspace",
@@ -98,6 +106,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "dg_m_grouped_gather": [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp],
             "dg_m_grouped_gather_weight_grad": [vp, vp, vp, vp, ci, ci, ci, ci, vp],
             "dg_lora_bf16_nt": [vp, ci, vp, vp, vp, vp, vp, ci, vp, ci, ci, ci, ci, ci, ci, vp],
+            "dg_route_balance": [vp, ci, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp],
+            "dg_route_balance_backward": [vp, ci, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp],
+            "dg_bf16_fp4_gemv_nt": [vp, ci, vp, vp, vp, ci, vp, ci, ci, ci, ci, vp],
+            "dg_bf16_int4_gemv_nt": [vp, ci, vp, vp, ci, vp, ci, vp, ci, vp, ci, ci, ci, ci, vp],
+            "dg_m_grouped_bf16_fp4_gemv_nt_topk": [vp, ci, ci, vp, vp, vp, vp, ci, vp, ci, ci, ci, ci, ci, ci, ci, vp],
+            "dg_m_grouped_bf16_int4_gemv_nt_topk": [vp, ci, ci, vp, vp, vp, ci, vp, ci, vp, ci, vp, ci, ci, ci, ci, ci,
+                                                    ci, ci, vp],
+            "dg_grad_norm": [vp, vp, vp, ci, vp, vp],
+            "dg_grad_clip": [vp, vp, vp, vp, ci, vp, cf, vp],
         }.items():
             getattr(lib, name).argtypes = types
             getattr(lib, name).restype = ci
@@ -560,3 +577,147 @@ def dg_lora_bf16_nt(x, a, b, scales, adapter_ids, c, d, stream=None) -> None:
             _ptr(scales, "scales", _F32, (L,), True), _ptr(adapter_ids, "adapter_ids", _I32, (T,)), pc, ldc, pd, ldd,
             T, N, K, R, L)
     _run("dg_lora_bf16_nt", dict(x=x, a=a, b=b, scales=scales, adapter_ids=adapter_ids, c=c, d=d), args, stream)
+
+
+def _starts(seq_starts, S):
+    return _ptr(seq_starts, "seq_starts", _I32, (S + 1,), S == 1)
+
+
+def dg_route_balance(logits, topk_ids, seq_starts, loss, counts, score="softmax", scale=1.0, stream=None) -> None:
+    """The router's balance loss per sequence, loss fp32 [S], and the experts' counts, int32 [S][E], of
+    logits [T][E] (fp32 or bf16) and topk_ids int32 [T][top_k]; seq_starts int32 [S + 1], or None for one sequence."""
+    T, E = _rank(logits, "logits", (2,))
+    k = _rank(topk_ids, "topk_ids", (2,))[1]
+    S = _rank(loss, "loss", (1,))[0]
+    args = (_ptr(logits, "logits", _LOGITS, None), 0 if logits.dtype == torch.float32 else 1,
+            _ptr(topk_ids, "topk_ids", _I32, (T, k)), _starts(seq_starts, S), _ptr(loss, "loss", _F32, None),
+            _ptr(counts, "counts", _I32, (S, E)), T, E, k, S, _score(score), float(scale))
+    _run("dg_route_balance", dict(logits=logits, topk_ids=topk_ids, seq_starts=seq_starts, loss=loss, counts=counts),
+         args, stream)
+
+
+def dg_route_balance_backward(logits, counts, seq_starts, grad_loss, c, grad_logits, top_k, score="softmax", scale=1.0,
+                              stream=None) -> None:
+    """grad_logits = c + the balance loss's gradient [T][E] (of the logits' type; c None: 0) for the forward call's
+    counts [S][E] and grad_loss fp32 [S] (None: ones)."""
+    T, E = _rank(logits, "logits", (2,))
+    S = _rank(counts, "counts", (2,))[0]
+    args = (_ptr(logits, "logits", _LOGITS, None), 0 if logits.dtype == torch.float32 else 1,
+            _ptr(counts, "counts", _I32, (S, E)), _starts(seq_starts, S),
+            _ptr(grad_loss, "grad_loss", _F32, (S,), True), _ptr(c, "c", (logits.dtype,), (T, E), True),
+            _ptr(grad_logits, "grad_logits", (logits.dtype,), (T, E)), T, E, int(top_k), S, _score(score),
+            float(scale))
+    _run("dg_route_balance_backward", dict(logits=logits, counts=counts, seq_starts=seq_starts, grad_loss=grad_loss,
+                                           c=c, grad_logits=grad_logits), args, stream)
+
+
+def _int4(b, scales, zeros, lead, N, K):
+    """(the C call's arguments of integer weights [*lead][N][K/2], by its tensors): the group size is K over the
+    scales' rows."""
+    rows = _rank(scales, "scales", (len(lead) + 2,))[-2]
+    if rows < 1 or K % rows != 0:
+        raise ValueError(f"scales has {rows} groups; they must divide K = {K}")
+    shape = (*lead, rows, N)
+    return (_ptr(b, "b", _U8, (*lead, N, K // 2)), _ptr(scales, "scales", _LOGITS, shape),
+            0 if scales.dtype == torch.float32 else 1, _ptr(zeros, "zeros", _U8, shape, True), K // rows)
+
+
+def _fp4(b, sfb, lead, N, K):
+    return _ptr(b, "b", _U8, (*lead, N, K // 2)), _ptr(sfb, "sfb", _I32, _sh(*lead, _kb(K), N))
+
+
+def dg_bf16_fp4_gemv_nt(x, b, sfb, c, d, stream=None) -> None:
+    """d[M][N] = bf16(c + x . dequant(b)^T) for a few tokens: x bf16 [M][K], b packed E2M1 [N][K/2], sfb int32
+    [K/128][N] (as dg_fp8_fp4_gemm_nt takes them), c (or None) and d bf16 [M][N].  The rows of x, c and d may lie
+    apart."""
+    M, K = _rank(x, "x", (2,))
+    N = _rank(b, "b", (2,))[0]
+    px, ldx = _strided(x, "x", (M, K))
+    pc, ldc = _strided(c, "c", (M, N), True)
+    pd, ldd = _strided(d, "d", (M, N))
+    args = (px, ldx, *_fp4(b, sfb, (), N, K), pc, ldc, pd, ldd, M, N, K)
+    _run("dg_bf16_fp4_gemv_nt", dict(x=x, b=b, sfb=sfb, c=c, d=d), args, stream)
+
+
+def dg_bf16_int4_gemv_nt(x, b, scales, zeros, c, d, stream=None) -> None:
+    """As dg_bf16_fp4_gemv_nt with integer weights: b [N][K/2] (two values of 0 to 15 per byte), scales fp32 or bf16
+    [K/group][N] with groups of 32, 64 or 128 values, zeros uint8 [K/group][N] or None (8)."""
+    M, K = _rank(x, "x", (2,))
+    N = _rank(b, "b", (2,))[0]
+    px, ldx = _strided(x, "x", (M, K))
+    pc, ldc = _strided(c, "c", (M, N), True)
+    pd, ldd = _strided(d, "d", (M, N))
+    args = (px, ldx, *_int4(b, scales, zeros, (), N, K), pc, ldc, pd, ldd, M, N, K)
+    _run("dg_bf16_int4_gemv_nt", dict(x=x, b=b, scales=scales, zeros=zeros, c=c, d=d), args, stream)
+
+
+def dg_m_grouped_bf16_fp4_gemv_nt_topk(x, topk_ids, first_expert, b, sfb, c, d, stream=None) -> None:
+    """The products of every choice with its expert's weights: topk_ids int32 [T][top_k], x bf16 [T][K] (a token's
+    choices share its row) or [T * top_k][K], b [G][N][K/2], sfb int32 [G][K/128][N], c (or None) and d bf16
+    [T * top_k][N]; a choice whose expert is not in [first_expert, first_expert + G) gets c, or zeros."""
+    T, k = _rank(topk_ids, "topk_ids", (2,))
+    rows, K = _rank(x, "x", (2,))
+    G, N, _ = _rank(b, "b", (3,))
+    px, ldx = _strided(x, "x", (rows, K))
+    pc, ldc = _strided(c, "c", (T * k, N), True)
+    pd, ldd = _strided(d, "d", (T * k, N))
+    args = (px, ldx, rows, _ptr(topk_ids, "topk_ids", _I32, None), *_fp4(b, sfb, (G,), N, K), pc, ldc, pd, ldd, T, k,
+            int(first_expert), G, N, K)
+    _run("dg_m_grouped_bf16_fp4_gemv_nt_topk", dict(x=x, topk_ids=topk_ids, b=b, sfb=sfb, c=c, d=d), args, stream)
+
+
+def dg_m_grouped_bf16_int4_gemv_nt_topk(x, topk_ids, first_expert, b, scales, zeros, c, d, stream=None) -> None:
+    """As dg_m_grouped_bf16_fp4_gemv_nt_topk with integer weights: b [G][N][K/2], scales fp32 or bf16 [G][K/group][N],
+    zeros uint8 [G][K/group][N] or None (8)."""
+    T, k = _rank(topk_ids, "topk_ids", (2,))
+    rows, K = _rank(x, "x", (2,))
+    G, N, _ = _rank(b, "b", (3,))
+    px, ldx = _strided(x, "x", (rows, K))
+    pc, ldc = _strided(c, "c", (T * k, N), True)
+    pd, ldd = _strided(d, "d", (T * k, N))
+    args = (px, ldx, rows, _ptr(topk_ids, "topk_ids", _I32, None), *_int4(b, scales, zeros, (G,), N, K), pc, ldc, pd,
+            ldd, T, k, int(first_expert), G, N, K)
+    _run("dg_m_grouped_bf16_int4_gemv_nt_topk", dict(x=x, topk_ids=topk_ids, b=b, scales=scales, zeros=zeros, c=c,
+                                                     d=d), args, stream)
+
+
+class GradList:
+    """Tensors (fp32 or bf16, contiguous, on one device) as the gradient calls take them, prepared once for gradients
+    that stay where they are: the list keeps their memory, not the tensor objects, and speaks of it whatever these
+    become later."""
+
+    def __init__(self, tensors):
+        self.tensors = [t.detach() if isinstance(t, torch.Tensor) else t for t in tensors]
+        n = len(self.tensors)
+        for i, t in enumerate(self.tensors):
+            _ptr(t, f"tensor {i}", _LOGITS, None)
+        if any(t.get_device() != self.tensors[0].get_device() for t in self.tensors):
+            raise ValueError("the tensors must be on one device")
+        self.pointers = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
+        self.types = (ctypes.c_int * n)(*[0 if t.dtype == torch.float32 else 1 for t in self.tensors])
+        self.sizes = (ctypes.c_longlong * n)(*[t.numel() for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _grads(tensors):
+    return tensors if isinstance(tensors, GradList) else GradList(tensors)
+
+
+def dg_grad_norm(grads, norm, stream=None) -> None:
+    """norm fp32 [1] = the 2-norm of all tensors together: a sequence of fp32 and bf16 tensors, or a GradList."""
+    g = _grads(grads)
+    args = (g.pointers, g.types, g.sizes, len(g), _ptr(norm, "norm", _F32, (1,)))
+    _run("dg_grad_norm", dict(norm=norm, **({"grads": g.tensors[0]} if len(g) else {})), args, stream)
+
+
+def dg_grad_clip(grads, out, norm, max_norm, stream=None) -> None:
+    """out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), of the same types and sizes; out may be grads."""
+    g = _grads(grads)
+    o = g if out is grads else _grads(out)
+    if g.types[:] != o.types[:] or g.sizes[:] != o.sizes[:]:
+        raise ValueError("out must have the types and sizes of grads")
+    args = (g.pointers, o.pointers, g.types, g.sizes, len(g), _ptr(norm, "norm", _F32, (1,)), float(max_norm))
+    _run("dg_grad_clip", dict(norm=norm, **({"grads": g.tensors[0], "out": o.tensors[0]} if len(g) else {})), args,
+         stream)

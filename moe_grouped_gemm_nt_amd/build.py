@@ -26,6 +26,9 @@ SOURCES = {
     "route.hip": [],
     "expert_rows.hip": [],
     "lora.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "balance.hip": [],
+    "gemv4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "grads.hip": [],
 }
 
 # packed fp32 VALU forms are disabled on purpose: the kernels issue one fp32
