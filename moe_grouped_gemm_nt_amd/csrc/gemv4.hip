@@ -11,12 +11,10 @@
 namespace dg {
 namespace {
 
-constexpr int WAVES = 4;
-constexpr int THREADS = WAVES * 64;
 constexpr int kTile = 16;                // rows of d per workgroup: the columns of an MFMA
 // Up to here every workgroup finds its tile's choices itself; beyond, layout kernels
 // make lists.
-constexpr int kInlineChoices = 512;
+constexpr int kInlineChoices = 2048;
 
 struct GemvParams {
   const uint16_t* x;
@@ -33,7 +31,9 @@ struct GemvParams {
   int n;                   // choices, or rows of x
   int first, G;            // experts here: [first, first + G)
   int N, K;
-  int tile0, tiles, parts;
+  int tiles;               // tiles of choices, or the most there can be
+  long long item0;         // of tiles * parts, in this launch
+  int items;
   int scales_bf16;
   const int32_t* layout;   // lists (many choices): expert of each row, G = choices of other experts
   const int32_t* slot_of;  // choice of each row, -1 where a tile is not full
@@ -43,14 +43,18 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef u16x4 u16x4_u __attribute__((aligned(2)));               // at any address of its elements
 
-// The choices of this workgroup's tile into rows[kTile] (-1 where there is none) and
-// their expert into *id (-1: none here).  Returns false for a workgroup without a
-// tile.  Ends with a barrier.
+// The choices of tile `tile` into rows[kTile] (-1 where there is none) and their
+// expert into *id (-1: none here).  Returns false where there is no such tile.  Ends
+// with a barrier.
 //
-// Without lists, the workgroup of choice t has a tile if the choices before t hold a
-// multiple of 16 of t's expert; its tile is t and the next ones of that expert.
-__device__ __forceinline__ bool find_tile(const GemvParams& p, int tile, int* rows, int* id) {
+// Without lists every workgroup counts the experts' choices in LDS (`room`), so that
+// the tiles are numbered by expert without gaps and few workgroups find none, and
+// takes its sixteen in the order of the choices.
+template <int THREADS>
+__device__ __forceinline__ bool find_tile(const GemvParams& p, int tile, int* rows, int* id, int* room) {
   if (!p.ids) {
     *id = 0;
     const int i = tile * kTile + (int)threadIdx.x;
@@ -64,27 +68,48 @@ __device__ __forceinline__ bool find_tile(const GemvParams& p, int tile, int* ro
       rows[threadIdx.x] = i < 0 ? -1 : p.i0 + i;
     }
   } else {
-    const int lane = threadIdx.x & 63;
-    auto key = [&](int v) { return v >= p.first && v - p.first < p.G ? v - p.first : -1; };
-    int ids[kInlineChoices / 64];
-#pragma unroll
-    for (int i = 0; i < kInlineChoices / 64; ++i) ids[i] = i * 64 + lane < p.n ? key(p.ids[i * 64 + lane]) : -2;
-    const int mine = key(p.ids[tile]);
+    int* count = room;                                           // [G + 1], the last of choices that are not here
+    int16_t* group = reinterpret_cast<int16_t*>(room + kMaxLayoutGroups + 1);            // [n]
+    for (int g = threadIdx.x; g <= p.G; g += THREADS) count[g] = 0;
     if (threadIdx.x < kTile) rows[threadIdx.x] = -1;
     __syncthreads();
-    int before = 0, after = 0;
-#pragma unroll
-    for (int i = 0; i < kInlineChoices / 64; ++i) {
-      if (i * 64 >= p.n) break;
-      const int s = i * 64 + lane;
-      before += __popcll(__ballot(ids[i] == mine && s < tile));
-      const uint64_t m = __ballot(ids[i] == mine && s >= tile);
-      const int at = after + __popcll(m & ((1ull << lane) - 1));
-      if (ids[i] == mine && s >= tile && at < kTile && threadIdx.x < 64) rows[at] = p.i0 + s;
-      after += __popcll(m);
+    for (int i = threadIdx.x; i < p.n; i += THREADS) {
+      const long long e = (long long)p.ids[i] - p.first;
+      const int g = e >= 0 && e < p.G ? (int)e : p.G;
+      group[i] = (int16_t)g;
+      atomicAdd(&count[g], 1);
     }
-    *id = mine;
-    if (before % kTile != 0) return false;
+    __syncthreads();
+    const int lane = threadIdx.x & 63;
+    int before = 0, mine = -1, at = 0;                           // tiles of the groups so far; the tile's group and place
+    for (int base = 0; base <= p.G && mine < 0; base += 64) {
+      const int tiles = base + lane <= p.G ? (count[base + lane] + kTile - 1) / kTile : 0;
+      int upto = tiles;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(upto, o);
+        upto += lane >= o ? v : 0;
+      }
+      const uint64_t past = __ballot(before + upto > tile);
+      if (past) {
+        const int first = __ffsll((unsigned long long)past) - 1;
+        mine = base + first;
+        at = tile - before - __shfl(upto - tiles, first);
+      }
+      before += __shfl(upto, 63);
+    }
+    if (mine < 0) return false;
+    *id = mine < p.G ? mine : -1;
+    if (threadIdx.x < 64) {
+      int seen = -at * kTile;
+      for (int base = 0; base < p.n && seen < kTile; base += 64) {
+        const bool is = base + lane < p.n && group[base + lane] == mine;
+        const uint64_t m = __ballot(is);
+        const int to = seen + __popcll(m & ((1ull << lane) - 1));
+        if (is && to >= 0 && to < kTile) rows[to] = p.i0 + base + lane;
+        seen += __popcll(m);
+      }
+    }
   }
   __syncthreads();
   return true;
@@ -128,76 +153,238 @@ __device__ __forceinline__ bf16x8 even_first(u32x4 x) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
-__device__ __forceinline__ float load_scale(const GemvParams& p, size_t at) {
-  return p.scales_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p.scales)[at])
-                       : static_cast<const float*>(p.scales)[at];
-}
+// ---- the kernel ----------------------------------------------------------------
+// A workgroup has 16 * RT columns of d, as the MFMA's rows, for one tile of choices,
+// the MFMA's columns; its W waves take pieces of 256 K in turn, each with LDS of its
+// own (no barrier until the sums are joined).  Bound by reading the weights.
+//
+// A piece's rows of weights (one 128-byte line each) and of x come into LDS with
+// direct loads of whole lines, as many pieces at a time as there is room for, and
+// are read from there as MFMA operands.  (Operands loaded straight from memory,
+// sixteen rows at a time, occupy the CU's memory pipe for one cycle per row and
+// 16 bytes: 64 tokens of 8 of 128 experts, 32 of them here, of 4096 x 7168 took 307
+// us.)  A row's 16-byte chunk c lies at c ^ swz(row) (weights) or c ^ row (x).
+//
+// FORM 0: E2M1 codes, scaled as they are widened, so that one sum runs over K.
+// Otherwise the group size: a group's sum of q * x and its sum of x (a product with
+// ones) are joined and scaled when it ends.
+template <int FORM, int RT, int XL>
+struct Slot {
+  static constexpr int kWeights = RT * 2048;
+  static constexpr int kX = XL * 1024;                           // two rows of 256 values per load
+  static constexpr int kScales = FORM == 0 ? (RT < 2 ? 256 : RT * 128) : 256 / (FORM ? FORM : 1) * RT * 16 * 8;
+  static constexpr int kBytes = kWeights + kX + kScales;
+};
 
-// GROUP 0: E2M1 codes.  16 columns of d per workgroup, as the MFMA's rows, and the
-// tile's choices as its columns; the four waves take blocks of 128 K in turn.
-template <int GROUP>
-__global__ __launch_bounds__(THREADS) void gemv_kernel(GemvParams p) {
-  __shared__ int rows[kTile];
-  __shared__ f32x4 sums[WAVES][64];
-  int id;
-  const int tile = p.tile0 + (int)(blockIdx.x / p.parts), part = blockIdx.x % p.parts;
-  if (!find_tile(p, tile, rows, &id)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r16 = lane & 15, g16 = lane >> 4;
-  const int n0 = part * 16;
-  f32x4 acc = {};
-  if (id >= 0) {
-    const int n = min(n0 + r16, p.N - 1);                        // beyond N: not stored
-    const int i = rows[r16] >= 0 ? rows[r16] : rows[0];          // nor rows without a choice
-    const uint16_t* x = p.x + (size_t)(i / p.x_div) * p.ldx;
-    const uint8_t* b = p.b + ((size_t)id * p.N + n) * (p.K / 2);
-    for (int kb = wave; kb < p.K / 128; kb += WAVES) {
-      if constexpr (GROUP == 0) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(b + kb * 64 + g16 * 16);
-        const uint32_t e = (uint32_t)p.sfb[((size_t)id * (p.K / 128) + kb) * p.N + n];
-        const float scale = e8m0((e >> (8 * g16)) & 255);
+template <int FORM, int RT>
+constexpr int kWaveBytes = (Slot<FORM, RT, 8>::kBytes + 255) / 256 * 256;
+
+template <int FORM, int RT, int W, int XL>
+__device__ __forceinline__ void sum_pieces(const GemvParams& p, const int* rows, int id, int n0, int wave, uint8_t* own,
+                                           f32x4 (&acc)[RT]) {
+  typedef Slot<FORM, RT, XL> S;
+  constexpr int UP = kWaveBytes<FORM, RT> / S::kBytes < 4 ? kWaveBytes<FORM, RT> / S::kBytes : 4;
+  constexpr int ITEMS = FORM ? (256 / (FORM ? FORM : 1) * RT * 16 + 63) / 64 : 1;        // scales per lane and piece
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g16 = lane >> 4;
+  const int pieces = (p.K + 255) / 256;
+  const bool odd = (p.K & 128) != 0;           // the last piece is half as long: its second half repeats the first
+  const uint8_t* wsrc[2 * RT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8 xf = *reinterpret_cast<const bf16x8*>(x + (size_t)kb * 128 + g16 * 32 + j * 8);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_fp4(w[j], scale), xf, acc, 0, 0, 0);
+  for (int l = 0; l < 2 * RT; ++l)             // columns beyond N repeat the last: not stored
+    wsrc[l] = p.b + ((size_t)id * p.N + min(n0 + l * 8 + (lane >> 3), p.N - 1)) * (p.K / 2);
+  const uint16_t* xsrc[XL];
+#pragma unroll
+  for (int l = 0; l < XL; ++l) {
+    const int i = rows[2 * l + (lane >> 5)];   // a row without a choice repeats the first: not stored
+    xsrc[l] = p.x + (size_t)((i >= 0 ? i : rows[0]) / p.x_div) * p.ldx;
+  }
+  const uint32_t base = lds_u32(own);
+  for (int i = wave; i < pieces; i += W * UP) {
+    float sc[UP][ITEMS], zs[UP][ITEMS];
+#pragma unroll
+    for (int u = 0; u < UP; ++u) {
+      const int piece = i + u * W;
+      if (piece >= pieces) break;
+      const bool half = odd && piece == pieces - 1;
+      const uint32_t slot = __builtin_amdgcn_readfirstlane(base + u * S::kBytes);
+      if constexpr (FORM != 0) {
+        const size_t row0 = ((size_t)id * (p.K / FORM) + (size_t)piece * (256 / FORM)) * p.N;
+#pragma unroll
+        for (int t = 0; t < ITEMS; ++t) {
+          const int item = t * 64 + lane;
+          const int g = half ? (item / (16 * RT)) & (128 / FORM - 1) : (item / (16 * RT)) & (256 / FORM - 1);
+          const size_t at = row0 + (size_t)g * p.N + min(n0 + item % (16 * RT), p.N - 1);
+          sc[u][t] = p.scales_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p.scales)[at])
+                                   : static_cast<const float*>(p.scales)[at];
+          zs[u][t] = p.zeros ? (float)p.zeros[at] : 8.0f;
         }
       } else {
-        const bf16x8 ones = {(__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f,
-                             (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f};
-        f32x4 q = {}, xsum = {};
+        const int kb = piece * 2, row = lane % (16 * RT < 64 ? 16 * RT : 64);
+        if constexpr (RT < 4) {
+          const int h = half ? 0 : (lane / (16 * RT)) & 1;
+          dma_4(p.sfb + ((size_t)id * (p.K / 128) + kb + h) * p.N + min(n0 + row, p.N - 1),
+                __builtin_amdgcn_readfirstlane(slot + S::kWeights + S::kX));
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            dma_4(p.sfb + ((size_t)id * (p.K / 128) + kb + (half ? 0 : h)) * p.N + min(n0 + row, p.N - 1),
+                  __builtin_amdgcn_readfirstlane(slot + S::kWeights + S::kX + h * 256));
+        }
+      }
+#pragma unroll
+      for (int l = 0; l < 2 * RT; ++l) {
+        int chunk = (lane & 7) ^ swz(l * 8 + (lane >> 3));
+        chunk = half ? chunk & 3 : chunk;
+        dma_16_nt(wsrc[l] + (size_t)piece * 128 + chunk * 16, __builtin_amdgcn_readfirstlane(slot + l * 1024));
+      }
+#pragma unroll
+      for (int l = 0; l < XL; ++l) {
+        int chunk = (lane & 31) ^ (2 * l + (lane >> 5));
+        chunk = half ? chunk & 15 : chunk;
+        dma_16(xsrc[l] + (size_t)piece * 256 + chunk * 8,
+               __builtin_amdgcn_readfirstlane(slot + S::kWeights + l * 1024));
+      }
+    }
+    wait_vm_lgkm0<0>();
+    asm volatile("" ::: "memory");
+    if constexpr (FORM != 0) {
+#pragma unroll
+      for (int u = 0; u < UP; ++u) {
+        if (i + u * W >= pieces) break;
+        float2* to = reinterpret_cast<float2*>(own + u * S::kBytes + S::kWeights + S::kX);
+#pragma unroll
+        for (int t = 0; t < ITEMS; ++t)
+          if (t * 64 + lane < 256 / FORM * RT * 16) to[t * 64 + lane] = make_float2(sc[u][t], -sc[u][t] * zs[u][t]);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+#pragma unroll
+    for (int u = 0; u < UP; ++u) {
+      const int piece = i + u * W;
+      if (piece >= pieces) break;
+      const uint8_t* slot = own + u * S::kBytes;
+      const uint8_t* xs = slot + S::kWeights;
+      const int xrow = r16 & (2 * XL - 1);     // columns from 2 * XL on repeat others: not stored
+      f32x4 q[RT] = {}, xsum = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && odd && piece == pieces - 1) break;
+        u32x4 w[RT];
+        float scale[RT];
+        if constexpr (FORM == 0) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const int row = r * 16 + r16;
+            w[r] = *reinterpret_cast<const u32x4*>(slot + row * 128 + (((h * 4 + g16) ^ swz(row)) << 4));
+            const uint32_t e = reinterpret_cast<const uint32_t*>(xs + S::kX)[h * 16 * RT + row];
+            scale[r] = e8m0((e >> (8 * g16)) & 255);
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(b + kb * 64 + j * 16 + g16 * 4);
-          const bf16x8 xf = even_first(*reinterpret_cast<const u32x4*>(x + (size_t)kb * 128 + j * 32 + g16 * 8));
-          q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_int4(w), xf, q, 0, 0, 0);
-          xsum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf, xsum, 0, 0, 0);
-          if ((j + 1) * 32 % GROUP == 0) {
-            const size_t at = ((size_t)id * (p.K / GROUP) + (kb * 128 + j * 32) / GROUP) * p.N;
+          // K of lane group g: codes g * 32 + j * 8 of a block, integers j * 32 + g * 8
+          const int chunk = FORM == 0 ? (h * 4 + g16) * 4 + j : (h * 4 + j) * 4 + g16;
+          const u32x4 xv = *reinterpret_cast<const u32x4*>(xs + xrow * 512 + ((chunk ^ xrow) << 4));
+          if constexpr (FORM == 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int m = min(n0 + g16 * 4 + e, p.N - 1);
-              const float zero = p.zeros ? (float)p.zeros[at + m] : 8.0f;
-              acc[e] = fmaf(load_scale(p, at + m), fmaf(-zero, xsum[e], q[e]), acc[e]);
+            for (int r = 0; r < RT; ++r)
+              acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_fp4(w[r][j], scale[r]),
+                                                               __builtin_bit_cast(bf16x8, xv), acc[r], 0, 0, 0);
+          } else {
+            const bf16x8 ones = {(__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f,
+                                 (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f};
+            const bf16x8 xf = even_first(xv);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              const int row = r * 16 + r16;
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(slot + row * 128 + (((h * 4 + j) ^ swz(row)) << 4) +
+                                                                    g16 * 4);
+              q[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_int4(v), xf, q[r], 0, 0, 0);
             }
-            q = f32x4{};
-            xsum = f32x4{};
+            xsum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf, xsum, 0, 0, 0);
+            constexpr int STEPS = FORM ? FORM / 32 : 1;
+            if ((j + 1) % STEPS == 0) {
+              const int g = (h * 4 + j) / STEPS;
+#pragma unroll
+              for (int r = 0; r < RT; ++r) {
+                const f32x4* s = reinterpret_cast<const f32x4*>(xs + S::kX + (g * 16 * RT + r * 16 + g16 * 4) * 8);
+                const f32x4 s0 = s[0], s1 = s[1];
+                acc[r][0] = fmaf(s0[1], xsum[0], fmaf(s0[0], q[r][0], acc[r][0]));
+                acc[r][1] = fmaf(s0[3], xsum[0], fmaf(s0[2], q[r][1], acc[r][1]));
+                acc[r][2] = fmaf(s1[1], xsum[0], fmaf(s1[0], q[r][2], acc[r][2]));
+                acc[r][3] = fmaf(s1[3], xsum[0], fmaf(s1[2], q[r][3], acc[r][3]));
+                q[r] = f32x4{};
+              }
+              xsum = f32x4{};
+            }
           }
         }
       }
     }
+    wait_vm_lgkm0<0>();                        // the slots are read before the next round fills them
+    asm volatile("" ::: "memory");
   }
-  sums[wave][lane] = acc;
-  __syncthreads();
-  // thread: choice threadIdx.x / 16, column threadIdx.x % 16
-  const int at = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
-  const int i = rows[at];
-  if (i < 0 || n >= p.N) return;
-  float v = p.c ? bf16_to_f32(p.c[(size_t)i * p.ldc + n]) : 0.0f;
-  const int from = ((threadIdx.x & 15) >> 2) * 16 + at, e = threadIdx.x & 3;
-  float sum = 0.0f;
+}
+
+template <int FORM, int RT, int W>
+__global__ __launch_bounds__(W * 64) void gemv_kernel(GemvParams p) {
+  __shared__ int rows[kTile];
+  __shared__ __attribute__((aligned(128))) uint8_t lds[W][kWaveBytes<FORM, RT>];
+  static_assert(sizeof(lds) >= (kMaxLayoutGroups + 1) * 4 + kInlineChoices * 2, "find_tile's room");
+  // consecutive workgroups go to the 8 XCDs in turn: each takes a run of items, the
+  // tiles of the same columns next to one another, for those that share an expert
+  const int per = (p.items + 7) / 8;
+  const int item = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || item >= p.items) return;
+  const int part = (int)((p.item0 + item) / p.tiles), tile = (int)(p.item0 + item - (long long)part * p.tiles);
+  int id;
+  if (!find_tile<W * 64>(p, tile, rows, &id, reinterpret_cast<int*>(&lds[0][0]))) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g16 = lane >> 4;
+  const int n0 = part * 16 * RT;
+  f32x4 acc[RT] = {};
+  if (id >= 0) {
+    if (rows[8] >= 0)
+      sum_pieces<FORM, RT, W, 8>(p, rows, id, n0, wave, lds[wave], acc);
+    else if (rows[4] >= 0)
+      sum_pieces<FORM, RT, W, 4>(p, rows, id, n0, wave, lds[wave], acc);
+    else if (rows[2] >= 0)
+      sum_pieces<FORM, RT, W, 2>(p, rows, id, n0, wave, lds[wave], acc);
+    else
+      sum_pieces<FORM, RT, W, 1>(p, rows, id, n0, wave, lds[wave], acc);
+    f32x4* sums = reinterpret_cast<f32x4*>(lds[wave]);
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) sum += sums[w][from][e];
-  p.d[(size_t)i * p.ldd + n] = f32_to_bf16(v + sum);
+    for (int r = 0; r < RT; ++r) sums[r * 64 + lane] = acc[r];
+    __syncthreads();
+  }
+  const int i = rows[r16];
+  if (i < 0) return;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    if (r % W != wave) continue;               // the waves share the sixteenths of the columns
+    const int n = n0 + r * 16 + g16 * 4;
+    if (n >= p.N) continue;
+    f32x4 sum = {};
+    if (id >= 0)
+#pragma unroll
+      for (int w = 0; w < W; ++w) sum += reinterpret_cast<const f32x4*>(lds[w])[r * 64 + lane];
+    const uint16_t* c = p.c ? p.c + (size_t)i * p.ldc + n : nullptr;
+    uint16_t* d = p.d + (size_t)i * p.ldd + n;
+    if (n + 4 <= p.N) {
+      u16x4 v = {};
+      if (c) v = *reinterpret_cast<const u16x4_u*>(c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = id >= 0 ? f32_to_bf16(bf16_to_f32(v[e]) + sum[e]) : v[e];
+      *reinterpret_cast<u16x4_u*>(d) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (n + e < p.N) {
+          const uint16_t v = c ? c[e] : 0;
+          d[e] = id >= 0 ? f32_to_bf16(bf16_to_f32(v) + sum[e]) : v;
+        }
+    }
+  }
 }
 
 constexpr long long kMaxChoices = 1LL << 30;
@@ -209,25 +396,30 @@ int launched() {
   return e == hipSuccess ? DG_OK : fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
 }
 
-int launch_tiles(GemvParams p, int group, long long tiles, hipStream_t st) {
-  p.parts = (p.N + 15) / 16;
-  const long long step = kMostGroups / p.parts;
-  for (long long t = 0; t < tiles; t += step) {
-    p.tile0 = (int)t;
-    p.tiles = (int)(tiles - t < step ? tiles - t : step);
-    const int grid = p.tiles * p.parts;
+template <int RT, int W>
+int launch_items(GemvParams p, int group, hipStream_t st) {
+  const long long items = (long long)p.tiles * ((p.N + 16 * RT - 1) / (16 * RT));
+  for (long long at = 0; at < items; at += p.items) {
+    p.item0 = at;
+    p.items = (int)(items - at < kMostGroups ? items - at : kMostGroups);
+    const int grid = (p.items + 7) / 8 * 8;
     if (group == 0)
-      gemv_kernel<0><<<grid, THREADS, 0, st>>>(p);
+      gemv_kernel<0, RT, W><<<grid, W * 64, 0, st>>>(p);
     else if (group == 32)
-      gemv_kernel<32><<<grid, THREADS, 0, st>>>(p);
+      gemv_kernel<32, RT, W><<<grid, W * 64, 0, st>>>(p);
     else if (group == 64)
-      gemv_kernel<64><<<grid, THREADS, 0, st>>>(p);
+      gemv_kernel<64, RT, W><<<grid, W * 64, 0, st>>>(p);
     else
-      gemv_kernel<128><<<grid, THREADS, 0, st>>>(p);
+      gemv_kernel<128, RT, W><<<grid, W * 64, 0, st>>>(p);
     const int s = launched();
     if (s != DG_OK) return s;
   }
   return DG_OK;
+}
+
+int launch_tiles(GemvParams p, int group, long long tiles, hipStream_t st) {
+  p.tiles = (int)tiles;
+  return launch_items<2, 4>(p, group, st);
 }
 
 // By choice: as many choices at a time as the scratch memory has room to list,
@@ -252,7 +444,9 @@ int launch_choices(GemvParams p, int group, int n, const int32_t* ids, hipStream
     p.ids = ids + i;
     p.layout = nullptr;
     p.slot_of = nullptr;
-    long long tiles = step;
+    // an expert's last tile may not be full
+    long long tiles = (groups < step ? groups : step) + step / kTile;
+    tiles = tiles < step ? tiles : step;
     if (step > kInlineChoices) {
       int32_t* layout = reinterpret_cast<int32_t*>(sc.ptr);
       LayoutParams lp{p.ids, step, p.first, (int)groups, kTile, 0, (int)rows, layout, nullptr, layout + rows, nullptr};
