@@ -11,7 +11,6 @@
 namespace dg {
 namespace {
 
-constexpr int kTile = 16;                // rows of d per workgroup: the columns of an MFMA
 // Up to here every workgroup finds its tile's choices itself; beyond, layout kernels
 // make lists.
 constexpr int kInlineChoices = 2048;
@@ -32,9 +31,11 @@ struct GemvParams {
   int first, G;            // experts here: [first, first + G)
   int N, K;
   int tiles;               // tiles of choices, or the most there can be
-  long long item0;         // of tiles * parts, in this launch
-  int items;
+  int others;              // tiles before them that look after choices of experts that are not here
+  int tile0, part0;        // first of this launch
+  int items;               // tiles * parts of this launch
   int scales_bf16;
+  int again;               // several tiles read the same weights
   const int32_t* layout;   // lists (many choices): expert of each row, G = choices of other experts
   const int32_t* slot_of;  // choice of each row, -1 where a tile is not full
 };
@@ -46,73 +47,115 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef u16x4 u16x4_u __attribute__((aligned(2)));               // at any address of its elements
 
-// The choices of tile `tile` into rows[kTile] (-1 where there is none) and their
-// expert into *id (-1: none here).  Returns false where there is no such tile.  Ends
-// with a barrier.
+// The local expert of an id, or -1
+__device__ __forceinline__ int local_expert(const GemvParams& p, int id) {
+  return id >= p.first && (unsigned)(id - p.first) < (unsigned)p.G ? id - p.first : -1;
+}
+
+__device__ __forceinline__ int wave_scan(int v) {                // sums over the lanes up to this one
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);          // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);          // row_bcast 15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);          // row_bcast 31 into rows 2 and 3
+  return v;
+}
+
+// The choices of tile `tile` into rows[16] (-1 where there is none) and their expert
+// into *id (-1: none here).  Returns false where there is no such tile.  Ends with a
+// barrier.
 //
 // Without lists every workgroup counts the experts' choices in LDS (`room`), so that
-// the tiles are numbered by expert without gaps and few workgroups find none, and
-// takes its sixteen in the order of the choices.
-template <int THREADS>
+// the tiles are numbered by expert without gaps and few workgroups find none.  An
+// expert's only tile takes its choices in whatever order they were counted (no
+// result depends on a choice's place in its tile), one of several its sixteen in
+// the order of the choices.
+template <int THREADS, int TILE>
 __device__ __forceinline__ bool find_tile(const GemvParams& p, int tile, int* rows, int* id, int* room) {
   if (!p.ids) {
     *id = 0;
-    const int i = tile * kTile + (int)threadIdx.x;
-    if (threadIdx.x < kTile) rows[threadIdx.x] = i < p.n ? i : -1;
+    const int i = tile * TILE + (int)threadIdx.x;
+    if (threadIdx.x < 16) rows[threadIdx.x] = threadIdx.x < TILE && i < p.n ? i : -1;
   } else if (p.layout) {
-    const int g = p.layout[(size_t)tile * kTile];
+    const int g = p.layout[(size_t)tile * TILE];
     if (g < 0) return false;
     *id = g < p.G ? g : -1;
-    if (threadIdx.x < kTile) {
-      const int i = p.slot_of[(size_t)tile * kTile + threadIdx.x];
+    if (threadIdx.x < 16) {
+      const int i = threadIdx.x < TILE ? p.slot_of[(size_t)tile * TILE + threadIdx.x] : -1;
       rows[threadIdx.x] = i < 0 ? -1 : p.i0 + i;
     }
   } else {
-    int* count = room;                                           // [G + 1], the last of choices that are not here
-    int16_t* group = reinterpret_cast<int16_t*>(room + kMaxLayoutGroups + 1);            // [n]
-    for (int g = threadIdx.x; g <= p.G; g += THREADS) count[g] = 0;
-    if (threadIdx.x < kTile) rows[threadIdx.x] = -1;
+    constexpr int MOST = kInlineChoices / THREADS;
+    int* count = room;                                           // [G]
+    int e[MOST], place[MOST];
+#pragma unroll
+    for (int j = 0; j < MOST; ++j) {
+      const int i = threadIdx.x + j * THREADS;
+      e[j] = i < p.n ? p.ids[i] : -1;
+    }
+    for (int g = threadIdx.x; g < p.G; g += THREADS) count[g] = 0;
+    if (threadIdx.x < 16) rows[threadIdx.x] = -1;
     __syncthreads();
-    for (int i = threadIdx.x; i < p.n; i += THREADS) {
-      const long long e = (long long)p.ids[i] - p.first;
-      const int g = e >= 0 && e < p.G ? (int)e : p.G;
-      group[i] = (int16_t)g;
-      atomicAdd(&count[g], 1);
+#pragma unroll
+    for (int j = 0; j < MOST; ++j) {
+      if (j * THREADS >= p.n) break;
+      e[j] = local_expert(p, e[j]);
+      if (e[j] >= 0) place[j] = atomicAdd(&count[e[j]], 1);
     }
     __syncthreads();
     const int lane = threadIdx.x & 63;
-    int before = 0, mine = -1, at = 0;                           // tiles of the groups so far; the tile's group and place
-    for (int base = 0; base <= p.G && mine < 0; base += 64) {
-      const int tiles = base + lane <= p.G ? (count[base + lane] + kTile - 1) / kTile : 0;
-      int upto = tiles;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(upto, o);
-        upto += lane >= o ? v : 0;
-      }
+    int before = 0, mine = -1, at = 0;                           // tiles of the experts so far; the tile's expert and place
+    for (int base = 0; base < p.G && mine < 0; base += 64) {
+      const int tiles = base + lane < p.G ? (count[base + lane] + TILE - 1) / TILE : 0;
+      const int upto = wave_scan(tiles);
       const uint64_t past = __ballot(before + upto > tile);
       if (past) {
         const int first = __ffsll((unsigned long long)past) - 1;
         mine = base + first;
-        at = tile - before - __shfl(upto - tiles, first);
+        at = tile - before - __builtin_amdgcn_readlane(upto - tiles, first);
       }
-      before += __shfl(upto, 63);
+      before += __builtin_amdgcn_readlane(upto, 63);
     }
     if (mine < 0) return false;
-    *id = mine < p.G ? mine : -1;
-    if (threadIdx.x < 64) {
-      int seen = -at * kTile;
-      for (int base = 0; base < p.n && seen < kTile; base += 64) {
-        const bool is = base + lane < p.n && group[base + lane] == mine;
+    *id = mine;
+    if (count[mine] <= TILE) {
+#pragma unroll
+      for (int j = 0; j < MOST; ++j) {
+        if (j * THREADS >= p.n) break;
+        if (e[j] == mine) rows[place[j]] = p.i0 + (int)threadIdx.x + j * THREADS;
+      }
+    } else if (threadIdx.x < 64) {
+      int seen = -at * TILE;
+      for (int base = 0; base < p.n && seen < TILE; base += 64) {
+        const bool is = base + lane < p.n && local_expert(p, p.ids[base + lane]) == mine;
         const uint64_t m = __ballot(is);
         const int to = seen + __popcll(m & ((1ull << lane) - 1));
-        if (is && to >= 0 && to < kTile) rows[to] = p.i0 + base + lane;
+        if (is && to >= 0 && to < TILE) rows[to] = p.i0 + base + lane;
         seen += __popcll(m);
       }
     }
   }
   __syncthreads();
   return true;
+}
+
+// Columns n0 .. n0 + columns - 1 of the choices of experts that are not here, of 64
+// choices from `first` on: c as it is, or zeros.
+template <int THREADS>
+__device__ __forceinline__ void write_others(const GemvParams& p, int first, int n0, int columns) {
+  for (int at = threadIdx.x; at < 64 * (columns / 4); at += THREADS) {
+    const int i = first + at / (columns / 4), n = n0 + at % (columns / 4) * 4;
+    if (i >= p.n || n >= p.N || local_expert(p, p.ids[i]) >= 0) continue;
+    const uint16_t* c = p.c ? p.c + (size_t)(p.i0 + i) * p.ldc + n : nullptr;
+    uint16_t* d = p.d + (size_t)(p.i0 + i) * p.ldd + n;
+    if (n + 4 <= p.N)
+      *reinterpret_cast<u16x4_u*>(d) = c ? *reinterpret_cast<const u16x4_u*>(c) : u16x4{};
+    else
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (n + e < p.N) d[e] = c ? c[e] : 0;
+  }
 }
 
 // ---- weights as MFMA operands ------------------------------------------------
@@ -172,202 +215,241 @@ template <int FORM, int RT, int XL>
 struct Slot {
   static constexpr int kWeights = RT * 2048;
   static constexpr int kX = XL * 1024;                           // two rows of 256 values per load
-  static constexpr int kScales = FORM == 0 ? (RT < 2 ? 256 : RT * 128) : 256 / (FORM ? FORM : 1) * RT * 16 * 8;
+  static constexpr int kScales = FORM != 0 ? 0 : RT < 2 ? 256 : RT * 128;            // E8M0 words of 16 * RT rows
   static constexpr int kBytes = kWeights + kX + kScales;
+  static constexpr int kLoads = 2 * RT + XL + (FORM != 0 ? 0 : RT < 4 ? 1 : RT / 2);
 };
-
+// Integers: a table of a piece's scales, as pairs (scale, -scale * zero point)
+template <int FORM>
+constexpr int kGroups = FORM ? 256 / (FORM ? FORM : 1) : 0;
 template <int FORM, int RT>
-constexpr int kWaveBytes = (Slot<FORM, RT, 8>::kBytes + 255) / 256 * 256;
+constexpr int kTable = kGroups<FORM> * 16 * RT * 8;
+// LDS of a wave: NS pieces of a full tile, more where it is not full
+template <int FORM, int RT, int TILE, int NS>
+constexpr int kWaveBytes = kTable<FORM, RT> + NS * Slot<FORM, RT, TILE / 2>::kBytes;
 
-template <int FORM, int RT, int W, int XL>
+template <int FORM, int RT, int W, int BW, int XL>
 __device__ __forceinline__ void sum_pieces(const GemvParams& p, const int* rows, int id, int n0, int wave, uint8_t* own,
                                            f32x4 (&acc)[RT]) {
   typedef Slot<FORM, RT, XL> S;
-  constexpr int UP = kWaveBytes<FORM, RT> / S::kBytes < 4 ? kWaveBytes<FORM, RT> / S::kBytes : 4;
-  constexpr int ITEMS = FORM ? (256 / (FORM ? FORM : 1) * RT * 16 + 63) / 64 : 1;        // scales per lane and piece
+  constexpr int GROUPS = kGroups<FORM>, TABLE = kTable<FORM, RT>;
+  constexpr int ITEMS = FORM ? (GROUPS * 16 * RT + 63) / 64 : 1; // scales per lane and piece
+  constexpr int FIT = (BW - TABLE) / S::kBytes;
+  constexpr int NS = FORM ? (FIT < 2 ? FIT : 2) : (FIT < 4 ? FIT : 4);
+  static_assert(NS >= 1 && NS * S::kLoads < 64, "slots");
   const int lane = threadIdx.x & 63, r16 = lane & 15, g16 = lane >> 4;
   const int pieces = (p.K + 255) / 256;
+  const int count = (pieces - wave + W - 1) / W;                 // this wave's: wave, wave + W, ...
+  if (count <= 0) return;
   const bool odd = (p.K & 128) != 0;           // the last piece is half as long: its second half repeats the first
-  const uint8_t* wsrc[2 * RT];
+  const int last = p.N - 1 - n0;               // columns beyond N repeat the last: not stored
+  const uint8_t* weights = p.b + ((size_t)id * p.N + n0) * (p.K / 2);
+  uint32_t wrow[2 * RT];
 #pragma unroll
-  for (int l = 0; l < 2 * RT; ++l)             // columns beyond N repeat the last: not stored
-    wsrc[l] = p.b + ((size_t)id * p.N + min(n0 + l * 8 + (lane >> 3), p.N - 1)) * (p.K / 2);
+  for (int l = 0; l < 2 * RT; ++l) wrow[l] = (uint32_t)min(l * 8 + (lane >> 3), last) * (uint32_t)(p.K / 2);
   const uint16_t* xsrc[XL];
 #pragma unroll
   for (int l = 0; l < XL; ++l) {
     const int i = rows[2 * l + (lane >> 5)];   // a row without a choice repeats the first: not stored
     xsrc[l] = p.x + (size_t)((i >= 0 ? i : rows[0]) / p.x_div) * p.ldx;
   }
-  const uint32_t base = lds_u32(own);
-  for (int i = wave; i < pieces; i += W * UP) {
-    float sc[UP][ITEMS], zs[UP][ITEMS];
-#pragma unroll
-    for (int u = 0; u < UP; ++u) {
-      const int piece = i + u * W;
-      if (piece >= pieces) break;
-      const bool half = odd && piece == pieces - 1;
-      const uint32_t slot = __builtin_amdgcn_readfirstlane(base + u * S::kBytes);
-      if constexpr (FORM != 0) {
-        const size_t row0 = ((size_t)id * (p.K / FORM) + (size_t)piece * (256 / FORM)) * p.N;
-#pragma unroll
-        for (int t = 0; t < ITEMS; ++t) {
-          const int item = t * 64 + lane;
-          const int g = half ? (item / (16 * RT)) & (128 / FORM - 1) : (item / (16 * RT)) & (256 / FORM - 1);
-          const size_t at = row0 + (size_t)g * p.N + min(n0 + item % (16 * RT), p.N - 1);
-          sc[u][t] = p.scales_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p.scales)[at])
-                                   : static_cast<const float*>(p.scales)[at];
-          zs[u][t] = p.zeros ? (float)p.zeros[at] : 8.0f;
-        }
+  const uint32_t base = lds_u32(own) + TABLE;
+  auto issue = [&](int k) {
+    const int piece = wave + k * W;
+    const bool half = odd && piece == pieces - 1;
+    const uint32_t slot = __builtin_amdgcn_readfirstlane(base + (k % NS) * S::kBytes);
+    if constexpr (FORM == 0) {
+      const int32_t* e = p.sfb + ((size_t)id * (p.K / 128) + piece * 2) * p.N + n0;
+      const uint32_t to = slot + S::kWeights + S::kX;
+      if constexpr (RT < 4) {                  // one load for both blocks
+        const int h = half ? 0 : (lane / (16 * RT)) & 1;
+        dma_4(e + (size_t)h * p.N + min(lane % (16 * RT), last), __builtin_amdgcn_readfirstlane(to));
       } else {
-        const int kb = piece * 2, row = lane % (16 * RT < 64 ? 16 * RT : 64);
-        if constexpr (RT < 4) {
-          const int h = half ? 0 : (lane / (16 * RT)) & 1;
-          dma_4(p.sfb + ((size_t)id * (p.K / 128) + kb + h) * p.N + min(n0 + row, p.N - 1),
-                __builtin_amdgcn_readfirstlane(slot + S::kWeights + S::kX));
-        } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            dma_4(p.sfb + ((size_t)id * (p.K / 128) + kb + (half ? 0 : h)) * p.N + min(n0 + row, p.N - 1),
-                  __builtin_amdgcn_readfirstlane(slot + S::kWeights + S::kX + h * 256));
+        for (int l = 0; l < RT / 2; ++l) {
+          const int h = half ? 0 : l / (RT / 4), row = l % (RT / 4) * 64 + lane;
+          dma_4(e + (size_t)h * p.N + min(row, last), __builtin_amdgcn_readfirstlane(to + l * 256));
+        }
+      }
+    }
+    const uint8_t* w = weights + (size_t)piece * 128;
+#pragma unroll
+    for (int l = 0; l < 2 * RT; ++l) {
+      int chunk = (lane & 7) ^ swz(l * 8 + (lane >> 3));
+      chunk = half ? chunk & 3 : chunk;
+      if (p.again)
+        dma_16s(w, wrow[l] + chunk * 16, __builtin_amdgcn_readfirstlane(slot + l * 1024));
+      else
+        dma_16s_nt(w, wrow[l] + chunk * 16, __builtin_amdgcn_readfirstlane(slot + l * 1024));
+    }
+#pragma unroll
+    for (int l = 0; l < XL; ++l) {
+      int chunk = (lane & 31) ^ (2 * l + (lane >> 5));
+      chunk = half ? chunk & 15 : chunk;
+      dma_16(xsrc[l] + (size_t)piece * 256 + chunk * 8,
+             __builtin_amdgcn_readfirstlane(slot + S::kWeights + l * 1024));
+    }
+  };
+  // integers: a piece's scales and zero points come through registers, as they are: a
+  // conversion here would wait for each of them
+  uint32_t sc[ITEMS], zs[ITEMS];
+  auto load_scales = [&](int k) {
+    if constexpr (FORM != 0) {
+      const int piece = wave + k * W;
+      const size_t at = ((size_t)id * (p.K / FORM) + (size_t)piece * GROUPS) * p.N + n0;
+      const int mask = odd && piece == pieces - 1 ? GROUPS / 2 - 1 : GROUPS - 1;
+#pragma unroll
+      for (int t = 0; t < ITEMS; ++t) {
+        const int item = t * 64 + lane;
+        const uint32_t off = (uint32_t)((item / (16 * RT)) & mask) * (uint32_t)p.N + (uint32_t)min(item % (16 * RT), last);
+        sc[t] = p.scales_bf16 ? (static_cast<const uint16_t*>(p.scales) + at)[off]
+                              : (static_cast<const uint32_t*>(p.scales) + at)[off];
+        zs[t] = p.zeros ? (p.zeros + at)[off] : 8;
+      }
+    }
+  };
+  if constexpr (FORM != 0) {
+    load_scales(0);
+    issue(0);
+  } else {
+    for (int k = 0; k < NS - 1 && k < count; ++k) issue(k);
+  }
+  for (int k = 0; k < count; ++k) {
+    if constexpr (FORM != 0) {
+      wait_vm_lgkm0<0>();
+      asm volatile("" ::: "memory");
+      float2* to = reinterpret_cast<float2*>(own);
+#pragma unroll
+      for (int t = 0; t < ITEMS; ++t) {
+        const float s = __uint_as_float(p.scales_bf16 ? sc[t] << 16 : sc[t]);
+        if (t * 64 + lane < GROUPS * 16 * RT) to[t * 64 + lane] = make_float2(s, -s * (float)zs[t]);
+      }
+      if (k + 1 < count) {
+        load_scales(k + 1);
+        if (NS > 1) issue(k + 1);
+      }
+    } else {
+      if (k + NS - 1 < count) issue(k + NS - 1);
+      // piece k is complete: only later ones may be under way
+      wait_stages<S::kLoads, NS - 1>(min(NS - 1, count - 1 - k));
+      asm volatile("" ::: "memory");
+    }
+    const uint8_t* slot = own + TABLE + (k % NS) * S::kBytes;
+    const uint8_t* xs = slot + S::kWeights;
+    const int xrow = r16 & (2 * XL - 1);       // rows of d from 2 * XL on repeat others: not stored
+    f32x4 q[RT] = {}, xsum = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && odd && wave + k * W == pieces - 1) break;
+      u32x4 w[RT];
+      float scale[RT];
+      if constexpr (FORM == 0) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const int row = r * 16 + r16;
+          w[r] = *reinterpret_cast<const u32x4*>(slot + row * 128 + (((h * 4 + g16) ^ swz(row)) << 4));
+          const uint32_t e = reinterpret_cast<const uint32_t*>(xs + S::kX)[h * 16 * RT + row];
+          scale[r] = e8m0((e >> (8 * g16)) & 255);
         }
       }
 #pragma unroll
-      for (int l = 0; l < 2 * RT; ++l) {
-        int chunk = (lane & 7) ^ swz(l * 8 + (lane >> 3));
-        chunk = half ? chunk & 3 : chunk;
-        dma_16_nt(wsrc[l] + (size_t)piece * 128 + chunk * 16, __builtin_amdgcn_readfirstlane(slot + l * 1024));
-      }
-#pragma unroll
-      for (int l = 0; l < XL; ++l) {
-        int chunk = (lane & 31) ^ (2 * l + (lane >> 5));
-        chunk = half ? chunk & 15 : chunk;
-        dma_16(xsrc[l] + (size_t)piece * 256 + chunk * 8,
-               __builtin_amdgcn_readfirstlane(slot + S::kWeights + l * 1024));
-      }
-    }
-    wait_vm_lgkm0<0>();
-    asm volatile("" ::: "memory");
-    if constexpr (FORM != 0) {
-#pragma unroll
-      for (int u = 0; u < UP; ++u) {
-        if (i + u * W >= pieces) break;
-        float2* to = reinterpret_cast<float2*>(own + u * S::kBytes + S::kWeights + S::kX);
-#pragma unroll
-        for (int t = 0; t < ITEMS; ++t)
-          if (t * 64 + lane < 256 / FORM * RT * 16) to[t * 64 + lane] = make_float2(sc[u][t], -sc[u][t] * zs[u][t]);
-      }
-      __builtin_amdgcn_wave_barrier();
-    }
-#pragma unroll
-    for (int u = 0; u < UP; ++u) {
-      const int piece = i + u * W;
-      if (piece >= pieces) break;
-      const uint8_t* slot = own + u * S::kBytes;
-      const uint8_t* xs = slot + S::kWeights;
-      const int xrow = r16 & (2 * XL - 1);     // columns from 2 * XL on repeat others: not stored
-      f32x4 q[RT] = {}, xsum = {};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == 1 && odd && piece == pieces - 1) break;
-        u32x4 w[RT];
-        float scale[RT];
+      for (int j = 0; j < 4; ++j) {
+        // K of lane group g: codes g * 32 + j * 8 of a block, integers j * 32 + g * 8
+        const int chunk = FORM == 0 ? (h * 4 + g16) * 4 + j : (h * 4 + j) * 4 + g16;
+        const u32x4 xv = *reinterpret_cast<const u32x4*>(xs + xrow * 512 + ((chunk ^ xrow) << 4));
         if constexpr (FORM == 0) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv), widen_fp4(w[r][j], scale[r]),
+                                                             acc[r], 0, 0, 0);
+        } else {
+          const bf16x8 ones = {(__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f,
+                               (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f};
+          const bf16x8 xf = even_first(xv);
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
             const int row = r * 16 + r16;
-            w[r] = *reinterpret_cast<const u32x4*>(slot + row * 128 + (((h * 4 + g16) ^ swz(row)) << 4));
-            const uint32_t e = reinterpret_cast<const uint32_t*>(xs + S::kX)[h * 16 * RT + row];
-            scale[r] = e8m0((e >> (8 * g16)) & 255);
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(slot + row * 128 + (((h * 4 + j) ^ swz(row)) << 4) +
+                                                                  g16 * 4);
+            q[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, widen_int4(v), q[r], 0, 0, 0);
           }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // K of lane group g: codes g * 32 + j * 8 of a block, integers j * 32 + g * 8
-          const int chunk = FORM == 0 ? (h * 4 + g16) * 4 + j : (h * 4 + j) * 4 + g16;
-          const u32x4 xv = *reinterpret_cast<const u32x4*>(xs + xrow * 512 + ((chunk ^ xrow) << 4));
-          if constexpr (FORM == 0) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-              acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_fp4(w[r][j], scale[r]),
-                                                               __builtin_bit_cast(bf16x8, xv), acc[r], 0, 0, 0);
-          } else {
-            const bf16x8 ones = {(__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f,
-                                 (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f};
-            const bf16x8 xf = even_first(xv);
+          xsum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, ones, xsum, 0, 0, 0);
+          constexpr int STEPS = FORM ? FORM / 32 : 1;
+          if ((j + 1) % STEPS == 0) {
+            const int g = (h * 4 + j) / STEPS;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-              const int row = r * 16 + r16;
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(slot + row * 128 + (((h * 4 + j) ^ swz(row)) << 4) +
-                                                                    g16 * 4);
-              q[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_int4(v), xf, q[r], 0, 0, 0);
-            }
-            xsum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf, xsum, 0, 0, 0);
-            constexpr int STEPS = FORM ? FORM / 32 : 1;
-            if ((j + 1) % STEPS == 0) {
-              const int g = (h * 4 + j) / STEPS;
+              const float2 s = reinterpret_cast<const float2*>(own)[g * 16 * RT + r * 16 + r16];
 #pragma unroll
-              for (int r = 0; r < RT; ++r) {
-                const f32x4* s = reinterpret_cast<const f32x4*>(xs + S::kX + (g * 16 * RT + r * 16 + g16 * 4) * 8);
-                const f32x4 s0 = s[0], s1 = s[1];
-                acc[r][0] = fmaf(s0[1], xsum[0], fmaf(s0[0], q[r][0], acc[r][0]));
-                acc[r][1] = fmaf(s0[3], xsum[0], fmaf(s0[2], q[r][1], acc[r][1]));
-                acc[r][2] = fmaf(s1[1], xsum[0], fmaf(s1[0], q[r][2], acc[r][2]));
-                acc[r][3] = fmaf(s1[3], xsum[0], fmaf(s1[2], q[r][3], acc[r][3]));
-                q[r] = f32x4{};
-              }
-              xsum = f32x4{};
+              for (int e = 0; e < (XL == 1 ? 2 : 4); ++e)        // (a lane's rows of d from 2 * XL on are not stored)
+                acc[r][e] = fmaf(s.y, xsum[e], fmaf(s.x, q[r][e], acc[r][e]));
+              q[r] = f32x4{};
             }
+            xsum = f32x4{};
           }
         }
       }
     }
-    wait_vm_lgkm0<0>();                        // the slots are read before the next round fills them
     asm volatile("" ::: "memory");
+    wait_vm_lgkm0<63>();                       // the slot is read before the next piece fills it
+    if (FORM != 0 && NS == 1 && k + 1 < count) issue(k + 1);
   }
 }
 
-template <int FORM, int RT, int W>
+template <int FORM, int RT, int W, int TILE, int NS>
 __global__ __launch_bounds__(W * 64) void gemv_kernel(GemvParams p) {
-  __shared__ int rows[kTile];
-  __shared__ __attribute__((aligned(128))) uint8_t lds[W][kWaveBytes<FORM, RT>];
-  static_assert(sizeof(lds) >= (kMaxLayoutGroups + 1) * 4 + kInlineChoices * 2, "find_tile's room");
+  constexpr int BW = kWaveBytes<FORM, RT, TILE, NS>;
+  __shared__ int rows[16];
+  __shared__ __attribute__((aligned(128))) uint8_t lds[W][BW];
+  static_assert(sizeof(lds) >= kMaxLayoutGroups * 4, "find_tile's room");
   // consecutive workgroups go to the 8 XCDs in turn: each takes a run of items, the
   // tiles of the same columns next to one another, for those that share an expert
   const int per = (p.items + 7) / 8;
   const int item = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per || item >= p.items) return;
-  const int part = (int)((p.item0 + item) / p.tiles), tile = (int)(p.item0 + item - (long long)part * p.tiles);
+  const int at = item / p.tiles, part = p.part0 + at, n0 = part * 16 * RT;
+  int tile = p.tile0 + item - at * p.tiles;
+  if (tile < p.others) {
+    write_others<W * 64>(p, tile * 64, n0, 16 * RT);
+    return;
+  }
+  tile -= p.others;
   int id;
-  if (!find_tile<W * 64>(p, tile, rows, &id, reinterpret_cast<int*>(&lds[0][0]))) return;
+  if (!find_tile<W * 64, TILE>(p, tile, rows, &id, reinterpret_cast<int*>(&lds[0][0]))) return;
+  id = __builtin_amdgcn_readfirstlane(id);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g16 = lane >> 4;
-  const int n0 = part * 16 * RT;
+  constexpr int OLD = 16 * RT + 4;             // a row of sums in LDS
+  static_assert(TILE * OLD * 4 <= BW, "sums");
   f32x4 acc[RT] = {};
   if (id >= 0) {
-    if (rows[8] >= 0)
-      sum_pieces<FORM, RT, W, 8>(p, rows, id, n0, wave, lds[wave], acc);
-    else if (rows[4] >= 0)
-      sum_pieces<FORM, RT, W, 4>(p, rows, id, n0, wave, lds[wave], acc);
-    else if (rows[2] >= 0)
-      sum_pieces<FORM, RT, W, 2>(p, rows, id, n0, wave, lds[wave], acc);
-    else
-      sum_pieces<FORM, RT, W, 1>(p, rows, id, n0, wave, lds[wave], acc);
-    f32x4* sums = reinterpret_cast<f32x4*>(lds[wave]);
+    if (TILE > 8 && rows[8] >= 0) {
+      if constexpr (TILE > 8) sum_pieces<FORM, RT, W, BW, 8>(p, rows, id, n0, wave, lds[wave], acc);
+    } else if (TILE > 4 && rows[4] >= 0) {
+      if constexpr (TILE > 4) sum_pieces<FORM, RT, W, BW, 4>(p, rows, id, n0, wave, lds[wave], acc);
+    } else if (rows[2] >= 0) {
+      sum_pieces<FORM, RT, W, BW, 2>(p, rows, id, n0, wave, lds[wave], acc);
+    } else {
+      sum_pieces<FORM, RT, W, BW, 1>(p, rows, id, n0, wave, lds[wave], acc);
+    }
+    // [row of d][column]
+    float* sums = reinterpret_cast<float*>(lds[wave]);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) sums[r * 64 + lane] = acc[r];
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (g16 * 4 + e < TILE) sums[(g16 * 4 + e) * OLD + r * 16 + r16] = acc[r][e];
     __syncthreads();
   }
-  const int i = rows[r16];
-  if (i < 0) return;
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    if (r % W != wave) continue;               // the waves share the sixteenths of the columns
-    const int n = n0 + r * 16 + g16 * 4;
-    if (n >= p.N) continue;
+  // thread: a row of d, four of its columns
+  for (int at4 = threadIdx.x; at4 < TILE * RT * 4; at4 += W * 64) {
+    const int row = at4 / (RT * 4), col = at4 % (RT * 4) * 4;
+    const int i = rows[row], n = n0 + col;
+    if (i < 0 || n >= p.N) continue;
     f32x4 sum = {};
     if (id >= 0)
 #pragma unroll
-      for (int w = 0; w < W; ++w) sum += reinterpret_cast<const f32x4*>(lds[w])[r * 64 + lane];
+      for (int w = 0; w < W; ++w) sum += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds[w]) + row * OLD + col);
     const uint16_t* c = p.c ? p.c + (size_t)i * p.ldc + n : nullptr;
     uint16_t* d = p.d + (size_t)i * p.ldd + n;
     if (n + 4 <= p.N) {
@@ -389,6 +471,7 @@ __global__ __launch_bounds__(W * 64) void gemv_kernel(GemvParams p) {
 
 constexpr long long kMaxChoices = 1LL << 30;
 constexpr int kMaxColumns = 1 << 20;
+constexpr int kMaxK = 1 << 24;           // a workgroup's rows of weights are addressed with 32 bits
 constexpr int kMostGroups = 1 << 22;     // workgroups per launch: a grid has fewer than 2^32 threads
 
 int launched() {
@@ -396,45 +479,71 @@ int launched() {
   return e == hipSuccess ? DG_OK : fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
 }
 
-template <int RT, int W>
-int launch_items(GemvParams p, int group, hipStream_t st) {
-  const long long items = (long long)p.tiles * ((p.N + 16 * RT - 1) / (16 * RT));
-  for (long long at = 0; at < items; at += p.items) {
-    p.item0 = at;
-    p.items = (int)(items - at < kMostGroups ? items - at : kMostGroups);
-    const int grid = (p.items + 7) / 8 * 8;
-    if (group == 0)
-      gemv_kernel<0, RT, W><<<grid, W * 64, 0, st>>>(p);
-    else if (group == 32)
-      gemv_kernel<32, RT, W><<<grid, W * 64, 0, st>>>(p);
-    else if (group == 64)
-      gemv_kernel<64, RT, W><<<grid, W * 64, 0, st>>>(p);
-    else
-      gemv_kernel<128, RT, W><<<grid, W * 64, 0, st>>>(p);
-    const int s = launched();
-    if (s != DG_OK) return s;
+template <int RT, int W, int TILE, int NS>
+int launch_items(GemvParams p, int group, long long tiles, hipStream_t st) {
+  const int parts = (p.N + 16 * RT - 1) / (16 * RT);
+  for (long long t = 0; t < tiles; t += p.tiles) {
+    p.tile0 = (int)t;
+    p.tiles = (int)(tiles - t < kMostGroups ? tiles - t : kMostGroups);
+    const int step = kMostGroups / p.tiles;
+    for (p.part0 = 0; p.part0 < parts; p.part0 += step) {
+      p.items = p.tiles * (parts - p.part0 < step ? parts - p.part0 : step);
+      const int grid = (p.items + 7) / 8 * 8;
+      if (group == 0)
+        gemv_kernel<0, RT, W, TILE, NS><<<grid, W * 64, 0, st>>>(p);
+      else if (group == 32)
+        gemv_kernel<32, (RT == 4 && W == 8 ? 2 : RT), W, TILE, NS><<<grid, W * 64, 0, st>>>(p);
+      else if (group == 64)
+        gemv_kernel<64, RT, W, TILE, NS><<<grid, W * 64, 0, st>>>(p);
+      else
+        gemv_kernel<128, RT, W, TILE, NS><<<grid, W * 64, 0, st>>>(p);
+      const int s = launched();
+      if (s != DG_OK) return s;
+    }
   }
   return DG_OK;
 }
 
-int launch_tiles(GemvParams p, int group, long long tiles, hipStream_t st) {
-  p.tiles = (int)tiles;
-  return launch_items<2, 4>(p, group, st);
+// Columns per workgroup (16 * RT), its waves W and the pieces NS that a wave has room
+// for, by how many workgroups per CU there would be.
+template <int TILE>
+int launch_tile(const GemvParams& p, int group, long long tiles, int num_cus, hipStream_t st) {
+  auto full = [&](int rt) { return tiles * ((p.N + 16 * rt - 1) / (16 * rt)) > num_cus; };
+  if constexpr (TILE == 16) {
+    if (full(4)) return launch_items<4, 4, TILE, 1>(p, group, tiles, st);
+    if (full(2) && group != 32) return launch_items<4, 8, TILE, 1>(p, group, tiles, st);
+    if (full(1)) return launch_items<2, 8, TILE, 1>(p, group, tiles, st);
+    return launch_items<1, 8, TILE, 1>(p, group, tiles, st);
+  } else {
+    if (full(2)) {
+      if (TILE == 4 && p.K > 4096) return launch_items<2, 4, TILE, 2>(p, group, tiles, st);
+      return launch_items<2, 4, TILE, 1>(p, group, tiles, st);
+    }
+    if (full(1)) return launch_items<2, 8, TILE, 2>(p, group, tiles, st);
+    return launch_items<1, 8, TILE, 2>(p, group, tiles, st);
+  }
+}
+
+// Tokens per tile: those of a small batch (an expert has no more of them, unless a
+// token's choices repeat it), which need less LDS for x
+int tile_of(int tokens) { return tokens <= 4 ? 4 : (tokens <= 8 ? 8 : 16); }
+
+int launch_tiles(const GemvParams& p, int group, int tile, long long tiles, int num_cus, hipStream_t st) {
+  if (tile == 4) return launch_tile<4>(p, group, tiles, num_cus, st);
+  if (tile == 8) return launch_tile<8>(p, group, tiles, num_cus, st);
+  return launch_tile<16>(p, group, tiles, num_cus, st);
 }
 
 // By choice: as many choices at a time as the scratch memory has room to list,
 // usually all, or kInlineChoices without lists.
-int launch_choices(GemvParams p, int group, int n, const int32_t* ids, hipStream_t st) {
-  Scratch sc;
-  int s = call_scratch(st, &sc);
-  if (s != DG_OK) return s;
+int launch_choices(GemvParams p, int group, int tile, int n, const int32_t* ids, const Scratch& sc, hipStream_t st) {
   const long long groups = p.G + 1;
   for (int i = 0; i < n;) {
     int step = n - i;
     size_t list_bytes = 0;
     long long rows = 0;
     while (step > kInlineChoices) {
-      rows = (step + (kTile - 1) * (groups < step ? groups : step)) / kTile * kTile;
+      rows = (step + (tile - 1) * (groups < step ? groups : step)) / tile * tile;
       list_bytes = (size_t)(2 * rows + 64) / 64 * 64 * sizeof(int32_t);
       if (list_bytes <= sc.bytes && rows < (1LL << 30)) break;
       step = step / 2 > kInlineChoices ? step / 2 : kInlineChoices;
@@ -444,20 +553,24 @@ int launch_choices(GemvParams p, int group, int n, const int32_t* ids, hipStream
     p.ids = ids + i;
     p.layout = nullptr;
     p.slot_of = nullptr;
-    // an expert's last tile may not be full
-    long long tiles = (groups < step ? groups : step) + step / kTile;
-    tiles = tiles < step ? tiles : step;
+    long long tiles;
     if (step > kInlineChoices) {
       int32_t* layout = reinterpret_cast<int32_t*>(sc.ptr);
-      LayoutParams lp{p.ids, step, p.first, (int)groups, kTile, 0, (int)rows, layout, nullptr, layout + rows, nullptr};
+      LayoutParams lp{p.ids, step, p.first, (int)groups, tile, 0, (int)rows, layout, nullptr, layout + rows, nullptr};
       lp.others = 1;
       const hipError_t e = launch_layout(lp, sc.ptr + list_bytes, sc.bytes - list_bytes, st);
       if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
       p.layout = layout;
       p.slot_of = layout + rows;
-      tiles = rows / kTile;
+      p.others = 0;
+      tiles = rows / tile;
+    } else {
+      // an expert's last tile may not be full
+      tiles = (p.G < step ? p.G : step) + step / tile;
+      p.others = (step + 63) / 64;
+      tiles = p.others + (tiles < step ? tiles : step);
     }
-    s = launch_tiles(p, group, tiles, st);
+    const int s = launch_tiles(p, group, tile, tiles, sc.num_cus, st);
     if (s != DG_OK) return s;
     i += step;
   }
@@ -469,6 +582,7 @@ int check_gemv(const GemvParams& p, long long rows, const void* scales, size_t s
   if (p.N < 0 || p.K < 0) return fail(DG_ERR_INVALID_ARG, "negative size (N=%d K=%d)", p.N, p.K);
   if (p.K % 128 != 0) return fail(DG_ERR_INVALID_ARG, "K=%d is not a multiple of 128", p.K);
   if (p.N > kMaxColumns) return fail(DG_ERR_UNSUPPORTED, "N=%d exceeds 2^20", p.N);
+  if (p.K > kMaxK) return fail(DG_ERR_UNSUPPORTED, "K=%d exceeds 2^24", p.K);
   if (rows == 0 || p.N == 0) return DG_OK;
   if (!p.d) return fail(DG_ERR_INVALID_ARG, "d must not be NULL");
   const bool terms = p.G > 0 && p.K > 0;                         // without them d = c
@@ -503,7 +617,13 @@ int dense(GemvParams& p, int group, int M, const void* scales, size_t scale_size
   p.n = M;
   const int s = check_gemv(p, M, scales, scale_size, ldx, ldc, ldd);
   if (s != DG_OK || M == 0 || p.N == 0) return s;
-  return launch_tiles(p, group, ((long long)M + kTile - 1) / kTile, static_cast<hipStream_t>(stream));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  Scratch sc;
+  const int e = call_scratch(st, &sc);
+  if (e != DG_OK) return e;
+  const int tile = tile_of(M);
+  p.again = M > tile;
+  return launch_tiles(p, group, tile, ((long long)M + tile - 1) / tile, sc.num_cus, st);
 }
 
 int by_choice(GemvParams& p, int group, int x_rows, const int32_t* ids, int T, int top_k, const void* scales,
@@ -522,7 +642,11 @@ int by_choice(GemvParams& p, int group, int x_rows, const int32_t* ids, int T, i
   if (n > 0 && p.N > 0 && (!ids || !aligned(ids, 4)))
     return fail(DG_ERR_INVALID_ARG, "topk_ids must be a 4-byte aligned address");
   if (n == 0 || p.N == 0) return DG_OK;
-  return launch_choices(p, group, (int)n, ids, static_cast<hipStream_t>(stream));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  Scratch sc;
+  s = call_scratch(st, &sc);
+  if (s != DG_OK) return s;
+  return launch_choices(p, group, tile_of(T), (int)n, ids, sc, st);
 }
 
 GemvParams operands(const void* x, int ldx, const void* b, const void* c, int ldc, void* d, int ldd, int N, int K) {
