@@ -5,6 +5,7 @@ HIP stream out.  Every step of the computation runs in the library's kernels;
 there is no fallback path.  A missing library raises at first use."""
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -681,43 +682,63 @@ def dg_m_grouped_bf16_int4_gemv_nt_topk(x, topk_ids, first_expert, b, scales, ze
                                                      d=d), args, stream)
 
 
+_GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _grad_arrays(tensors):
+    """(addresses, types, sizes) of fp32 and bf16 tensors that are contiguous and on the current device, as arrays
+    whose buffers the library reads during the call.  One pass per property: a loop over hundreds of small tensors
+    would take longer than the kernels."""
+    T = torch.Tensor
+    try:
+        types = array.array("i", [_GRAD_TYPES[t.dtype] for t in tensors])
+        fine = all(map(T.is_contiguous, tensors)) and len(set(map(T.get_device, tensors))) <= 1
+    except (TypeError, KeyError, AttributeError):
+        fine = False
+    if not fine:
+        for i, t in enumerate(tensors):
+            _ptr(t, f"tensor {i}", _LOGITS, None)
+        raise ValueError("the tensors must be on one device")
+    return array.array("Q", map(T.data_ptr, tensors)), types, array.array("q", map(T.numel, tensors))
+
+
 class GradList:
     """Tensors (fp32 or bf16, contiguous, on one device) as the gradient calls take them, prepared once for gradients
     that stay where they are: the list keeps their memory, not the tensor objects, and speaks of it whatever these
     become later."""
 
     def __init__(self, tensors):
-        self.tensors = [t.detach() if isinstance(t, torch.Tensor) else t for t in tensors]
-        n = len(self.tensors)
-        for i, t in enumerate(self.tensors):
-            _ptr(t, f"tensor {i}", _LOGITS, None)
-        if any(t.get_device() != self.tensors[0].get_device() for t in self.tensors):
-            raise ValueError("the tensors must be on one device")
-        self.pointers = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
-        self.types = (ctypes.c_int * n)(*[0 if t.dtype == torch.float32 else 1 for t in self.tensors])
-        self.sizes = (ctypes.c_longlong * n)(*[t.numel() for t in self.tensors])
+        tensors = list(tensors)
+        self.arrays = _grad_arrays(tensors)
+        self.tensors = [t.detach() for t in tensors]
 
     def __len__(self):
         return len(self.tensors)
 
 
 def _grads(tensors):
-    return tensors if isinstance(tensors, GradList) else GradList(tensors)
+    """(arrays, one of the tensors or None) of a GradList or a sequence of tensors"""
+    if isinstance(tensors, GradList):
+        return tensors.arrays, tensors.tensors[0] if tensors.tensors else None
+    if not isinstance(tensors, (list, tuple)):
+        tensors = list(tensors)
+    return _grad_arrays(tensors), tensors[0] if tensors else None
 
 
 def dg_grad_norm(grads, norm, stream=None) -> None:
     """norm fp32 [1] = the 2-norm of all tensors together: a sequence of fp32 and bf16 tensors, or a GradList."""
-    g = _grads(grads)
-    args = (g.pointers, g.types, g.sizes, len(g), _ptr(norm, "norm", _F32, (1,)))
-    _run("dg_grad_norm", dict(norm=norm, **({"grads": g.tensors[0]} if len(g) else {})), args, stream)
+    (pointers, types, sizes), one = _grads(grads)
+    args = (pointers.buffer_info()[0], types.buffer_info()[0], sizes.buffer_info()[0], len(types),
+            _ptr(norm, "norm", _F32, (1,)))
+    _run("dg_grad_norm", dict(grads=one, norm=norm), args, stream)
 
 
 def dg_grad_clip(grads, out, norm, max_norm, stream=None) -> None:
     """out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), of the same types and sizes; out may be grads."""
-    g = _grads(grads)
-    o = g if out is grads else _grads(out)
-    if g.types[:] != o.types[:] or g.sizes[:] != o.sizes[:]:
+    (pointers, types, sizes), one = _grads(grads)
+    (out_pointers, out_types, out_sizes), two = (((pointers, types, sizes), one) if out is grads else _grads(out))
+    if types != out_types or sizes != out_sizes:
         raise ValueError("out must have the types and sizes of grads")
-    args = (g.pointers, o.pointers, g.types, g.sizes, len(g), _ptr(norm, "norm", _F32, (1,)), float(max_norm))
-    _run("dg_grad_clip", dict(norm=norm, **({"grads": g.tensors[0], "out": o.tensors[0]} if len(g) else {})), args,
-         stream)
+    args = (pointers.buffer_info()[0], out_pointers.buffer_info()[0], types.buffer_info()[0], sizes.buffer_info()[0],
+            len(types), _ptr(norm, "norm", _F32, (1,)), float(max_norm))
+    _run("dg_grad_clip", dict(grads=one, out=two, norm=norm), args, stream)

@@ -56,45 +56,75 @@ __device__ __forceinline__ int tensor_of(const Grads& g, int c) {
   return lo;
 }
 
+constexpr int DEPTH = kChunk / (THREADS * 16);                   // 16-byte pieces per thread and chunk
+
+// Calls f(tensor, its chunk) for this workgroup's chunks
+template <typename F>
+__device__ __forceinline__ void each_chunk(const Grads& g, F f) {
+  int i = -1;
+  for (int c = blockIdx.x; c < g.start[g.n]; c += gridDim.x) {
+    if (i < 0) i = tensor_of(g, c);
+    while (c >= g.start[i + 1]) ++i;
+    f(i, c - g.start[i]);
+  }
+}
+
+// Elements of a 16-byte piece
+template <bool HALF>
+struct Piece {
+  typedef f32x4 V;
+  typedef f32x4_u U;
+  typedef float E;
+  static constexpr int N = 4;
+};
+template <>
+struct Piece<true> {
+  typedef Piece16<8>::V V;
+  typedef u16x8_u U;
+  typedef uint16_t E;
+  static constexpr int N = 8;
+};
+
+__device__ __forceinline__ double square(double sum, float v) { return fma((double)v, (double)v, sum); }
+__device__ __forceinline__ double square(double sum, uint16_t v) { return square(sum, widen(v)); }
+
+template <bool HALF>
+__device__ __forceinline__ double chunk_squares(const Grads& g, int i, int chunk, double sum) {
+  typedef Piece<HALF> P;
+  const long long at = (long long)chunk * (kChunk / sizeof(typename P::E));
+  const typename P::E* x = static_cast<const typename P::E*>(g.in[i]) + at;
+  const long long n = g.size[i] - at;
+  if (n >= (long long)(kChunk / sizeof(typename P::E))) {
+    typename P::V v[DEPTH];
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j) v[j] = *reinterpret_cast<const typename P::U*>(x + (j * THREADS + threadIdx.x) * P::N);
+    __builtin_amdgcn_sched_barrier(0);                           // no sum before the last load is under way
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j)
+#pragma unroll
+      for (int e = 0; e < P::N; ++e) sum = square(sum, v[j][e]);
+    return sum;
+  }
+  const int whole = (int)n / P::N * P::N;
+  for (int e = threadIdx.x * P::N; e < whole; e += THREADS * P::N) {
+    const typename P::V v = *reinterpret_cast<const typename P::U*>(x + e);
+#pragma unroll
+    for (int j = 0; j < P::N; ++j) sum = square(sum, v[j]);
+  }
+  return whole + (int)threadIdx.x < n ? square(sum, x[whole + threadIdx.x]) : sum;
+}
+
 // Squares are summed in fp64, where those of the largest and the smallest fp32
 // values still differ from infinity and zero; one partial sum per workgroup, added
 // up in their order by the second kernel.
 __global__ __launch_bounds__(THREADS) void grad_squares_kernel(Grads g) {
   double sum = 0.0;
-  for (int c = blockIdx.x; c < g.start[g.n]; c += gridDim.x) {
-    const int i = tensor_of(g, c);
-    if (g.half[i / 32] >> (i % 32) & 1) {
-      const long long at = (long long)(c - g.start[i]) * (kChunk / 2);
-      const uint16_t* x = static_cast<const uint16_t*>(g.in[i]) + at;
-      const int n = (int)min(g.size[i] - at, (long long)(kChunk / 2));
-      const int whole = n / 8 * 8;
-#pragma unroll 4
-      for (int e = threadIdx.x * 8; e < whole; e += THREADS * 8) {
-        const u16x8_u v = *reinterpret_cast<const u16x8_u*>(x + e);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fma((double)widen(v[j]), (double)widen(v[j]), sum);
-      }
-      if (whole + (int)threadIdx.x < n) {
-        const double v = widen(x[whole + threadIdx.x]);
-        sum = fma(v, v, sum);
-      }
-    } else {
-      const long long at = (long long)(c - g.start[i]) * (kChunk / 4);
-      const float* x = static_cast<const float*>(g.in[i]) + at;
-      const int n = (int)min(g.size[i] - at, (long long)(kChunk / 4));
-      const int whole = n / 4 * 4;
-#pragma unroll 4
-      for (int e = threadIdx.x * 4; e < whole; e += THREADS * 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4_u*>(x + e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum = fma((double)v[j], (double)v[j], sum);
-      }
-      if (whole + (int)threadIdx.x < n) {
-        const double v = x[whole + threadIdx.x];
-        sum = fma(v, v, sum);
-      }
-    }
-  }
+  each_chunk(g, [&](int i, int chunk) {
+    if (g.half[i / 32] >> (i % 32) & 1)
+      sum = chunk_squares<true>(g, i, chunk, sum);
+    else
+      sum = chunk_squares<false>(g, i, chunk, sum);
+  });
   __shared__ double sums[THREADS / 64];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
@@ -122,41 +152,56 @@ __global__ __launch_bounds__(THREADS) void grad_norm_kernel(const double* partia
   }
 }
 
+__device__ __forceinline__ float scaled(float v, float factor) { return v * factor; }
+__device__ __forceinline__ uint16_t scaled(uint16_t v, float factor) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(widen(v) * factor));
+}
+
+template <bool HALF>
+__device__ __forceinline__ void chunk_scale(const Grads& g, int i, int chunk, float factor) {
+  typedef Piece<HALF> P;
+  const long long at = (long long)chunk * (kChunk / sizeof(typename P::E));
+  const typename P::E* x = static_cast<const typename P::E*>(g.in[i]) + at;
+  typename P::E* y = static_cast<typename P::E*>(g.out[i]) + at;
+  const long long n = g.size[i] - at;
+  if (n >= (long long)(kChunk / sizeof(typename P::E))) {
+    typename P::V v[DEPTH];                                      // all loads first: y may be x
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j)
+      v[j] = __builtin_nontemporal_load(reinterpret_cast<const typename P::U*>(x + (j * THREADS + threadIdx.x) * P::N));
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j) {
+#pragma unroll
+      for (int e = 0; e < P::N; ++e) v[j][e] = scaled(v[j][e], factor);
+      __builtin_nontemporal_store(v[j], reinterpret_cast<typename P::U*>(y + (j * THREADS + threadIdx.x) * P::N));
+    }
+    return;
+  }
+  const int whole = (int)n / P::N * P::N;
+  for (int e = threadIdx.x * P::N; e < whole; e += THREADS * P::N) {
+    typename P::V v = *reinterpret_cast<const typename P::U*>(x + e);
+#pragma unroll
+    for (int j = 0; j < P::N; ++j) v[j] = scaled(v[j], factor);
+    *reinterpret_cast<typename P::U*>(y + e) = v;
+  }
+  if (whole + (int)threadIdx.x < n) y[whole + threadIdx.x] = scaled(x[whole + threadIdx.x], factor);
+}
+
+// The chunks from last to first: the norm has just read the last ones, and up to the
+// last-level cache's 256 MB of them are still there.
 __global__ __launch_bounds__(THREADS) void grad_clip_kernel(Grads g) {
   const float norm = *g.norm;
   const float q = g.max_norm / (norm + 1e-6f);
   const float factor = q > 1.0f ? 1.0f : q;                      // a NaN stays one
-  for (int c = blockIdx.x; c < g.start[g.n]; c += gridDim.x) {
-    const int i = tensor_of(g, c);
-    if (factor == 1.0f && g.in[i] == g.out[i]) continue;         // as it is
-    if (g.half[i / 32] >> (i % 32) & 1) {
-      const long long at = (long long)(c - g.start[i]) * (kChunk / 2);
-      const uint16_t* x = static_cast<const uint16_t*>(g.in[i]) + at;
-      uint16_t* y = static_cast<uint16_t*>(g.out[i]) + at;
-      const int n = (int)min(g.size[i] - at, (long long)(kChunk / 2));
-      const int whole = n / 8 * 8;
-#pragma unroll 4
-      for (int e = threadIdx.x * 8; e < whole; e += THREADS * 8) {
-        u16x8_u v = *reinterpret_cast<const u16x8_u*>(x + e);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(widen(v[j]) * factor));
-        *reinterpret_cast<u16x8_u*>(y + e) = v;
-      }
-      if (whole + (int)threadIdx.x < n)
-        y[whole + threadIdx.x] =
-            __builtin_bit_cast(uint16_t, static_cast<__bf16>(widen(x[whole + threadIdx.x]) * factor));
-    } else {
-      const long long at = (long long)(c - g.start[i]) * (kChunk / 4);
-      const float* x = static_cast<const float*>(g.in[i]) + at;
-      float* y = static_cast<float*>(g.out[i]) + at;
-      const int n = (int)min(g.size[i] - at, (long long)(kChunk / 4));
-      const int whole = n / 4 * 4;
-#pragma unroll 4
-      for (int e = threadIdx.x * 4; e < whole; e += THREADS * 4)
-        *reinterpret_cast<f32x4_u*>(y + e) = *reinterpret_cast<const f32x4_u*>(x + e) * factor;
-      if (whole + (int)threadIdx.x < n) y[whole + threadIdx.x] = x[whole + threadIdx.x] * factor;
-    }
-  }
+  each_chunk(g, [&](int i, int chunk) {
+    if (factor == 1.0f && g.in[i] == g.out[i]) return;           // as it is
+    chunk = g.start[i + 1] - g.start[i] - 1 - chunk;
+    if (g.half[i / 32] >> (i % 32) & 1)
+      chunk_scale<true>(g, i, chunk, factor);
+    else
+      chunk_scale<false>(g, i, chunk, factor);
+  });
 }
 
 constexpr long long kMaxBytes = 1LL << 45;
@@ -182,6 +227,7 @@ int check_grads(const void* const* grads, const int* types, const long long* siz
 
 // Calls f with the arguments of each launch: up to kTensors tensors with something
 // in them, and no more chunks than an int counts (a larger tensor goes out in parts).
+// With `out`, from the last tensor to the first.
 template <typename F>
 int each_launch(const void* const* grads, void* const* out, const int* types, const long long* sizes, int n, F f) {
   constexpr int kMostChunks = 1 << 30;
@@ -191,7 +237,8 @@ int each_launch(const void* const* grads, void* const* out, const int* types, co
     if (g.n > 0 && s == DG_OK) s = f(g);
     g = Grads{};
   };
-  for (int i = 0; i < n && s == DG_OK; ++i) {
+  for (int j = 0; j < n && s == DG_OK; ++j) {
+    const int i = out ? n - 1 - j : j;
     const long long per = kChunk / (long long)size_of(types[i]);
     for (long long at = 0; at < sizes[i] && s == DG_OK;) {
       if (g.n == kTensors || g.start[g.n] == kMostChunks) flush();
