@@ -3,11 +3,14 @@
     y = shared projection of x (FP8 dense product) with low-rank adapters per request
     ids, weights = router(y);  d = y + sum_j weights_j * expert_{ids_j}(x)
 
-serve()  runs it for a batch of tokens, over the masked layout (decoding: nothing
-         depends on the host, so the step can be captured in a HIP graph) or the
-         contiguous one (prefill);
-train()  adds the gradients of a given d: the expert weights' (K-grouped product),
-         the router weights' and the router's logits'.
+serve()       runs it for a batch of tokens, over the masked layout (decoding: nothing
+              depends on the host, so the step can be captured in a HIP graph) or the
+              contiguous one (prefill);
+serve_few()   runs it for a few tokens on 4-bit weights and unquantised activations,
+              the experts straight from the router's choices;
+train()       adds the gradients of a given d: the expert weights' (K-grouped product),
+              the router weights' and the router's logits';
+train_step()  adds the router's balance loss to it, and clips all gradients together.
 
 Run as a program it checks both against float64 and prints the differences:
 python examples/moe_layer.py"""
@@ -36,12 +39,33 @@ def quantise_blocks(w):
     return q.to(torch.float8_e4m3fn).contiguous(), sf.contiguous()
 
 
+FP4 = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def quantise_fp4(w):
+    """Weights [..., N, K] as packed E2M1 codes with one power-of-two scale per 32 values of K (once, at load time):
+    (b uint8 [..., N, K/2], sfb int32 [..., K/128, N], the weights that these stand for)."""
+    *lead, N, K = w.shape
+    blocks = w.float().view(*lead, N, K // 32, 32)
+    amax = blocks.abs().amax(-1, keepdim=True).clamp_min(2.0 ** -100)
+    e = torch.floor(torch.log2(amax)) - 2                        # the largest value lies in [4, 8)
+    v = (blocks * torch.exp2(-e)).clamp(-6.0, 6.0)
+    levels = FP4.to(w.device)
+    code = torch.bucketize(v.abs(), (levels[1:] + levels[:-1]) / 2)
+    stand_for = (levels[code] * torch.sign(v) * torch.exp2(e)).view(*lead, N, K)
+    code = (code + 8 * (v < 0)).to(torch.uint8).view(*lead, N, K // 2, 2)
+    sf = (e + 127).to(torch.uint8).view(*lead, N, K // 128, 4).transpose(-3, -2).contiguous()
+    return (code[..., 0] | code[..., 1] << 4).contiguous(), sf.view(torch.int32).squeeze(-1).contiguous(), stand_for
+
+
 class MoELayer:
     """The weights of one layer: shared [H][H], router [E][H], experts [E][H][H], adapters [L][R][H] and [L][H][R]."""
 
     def __init__(self, shared, router, experts, lora_a, lora_b, top_k, groups=1, kept=1):
         self.shared, self.shared_sf = quantise_blocks(shared)
         self.experts, self.experts_sf = quantise_blocks(experts)
+        self.shared4, self.shared4_sf, _ = quantise_fp4(shared)
+        self.experts4, self.experts4_sf, _ = quantise_fp4(experts)
         self.router = router.t().contiguous().float()
         self.lora_a, self.lora_b = lora_a.to(torch.bfloat16), lora_b.to(torch.bfloat16)
         self.top_k, self.groups, self.kept = top_k, groups, kept
@@ -107,6 +131,37 @@ class MoELayer:
         d = torch.empty_like(y)
         dg.dg_m_grouped_gather(rows, row_of, weights, y, d)
         return d
+
+    def serve_few(self, x, adapter_ids):
+        """d [T][H] of a few tokens, on the 4-bit weights: six launches, no rows moved or quantised."""
+        T, H = x.shape
+        k = self.top_k
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        dg.dg_lora_bf16_nt(x, self.lora_a, self.lora_b, None, adapter_ids, None, y)
+        dg.dg_bf16_fp4_gemv_nt(x, self.shared4, self.shared4_sf, y, y)
+        _, ids, weights = self.route(y)
+        rows = torch.empty(T * k, H, dtype=torch.bfloat16, device=x.device)
+        dg.dg_m_grouped_bf16_fp4_gemv_nt_topk(x, ids, 0, self.experts4, self.experts4_sf, None, rows)
+        row_of = torch.arange(T * k, dtype=torch.int32, device=x.device).view(T, k)
+        d = torch.empty_like(y)
+        dg.dg_m_grouped_gather(rows, row_of, weights, y, d)
+        return d
+
+    def train_step(self, x, adapter_ids, grad_d, seq_starts=None, balance=0.01, max_norm=1.0):
+        """(d, {"experts", "logits"}: the clipped gradients with the balance loss's, their norm before, the loss per
+        sequence, the experts' counts)."""
+        d, grad_experts, grad_logits, (logits, ids, _, _) = self.train(x, adapter_ids, grad_d)
+        S = 1 if seq_starts is None else seq_starts.numel() - 1
+        loss = torch.empty(S, device=x.device)
+        counts = torch.empty(S, logits.shape[1], dtype=torch.int32, device=x.device)
+        dg.dg_route_balance(logits, ids, seq_starts, loss, counts, score="sigmoid", scale=balance)
+        dg.dg_route_balance_backward(logits, counts, seq_starts, None, grad_logits, grad_logits, self.top_k,
+                                     score="sigmoid", scale=balance)
+        norm = torch.empty(1, device=x.device)
+        grads = [grad_experts, grad_logits]
+        dg.dg_grad_norm(grads, norm)
+        dg.dg_grad_clip(grads, grads, norm, max_norm)
+        return d, {"experts": grad_experts, "logits": grad_logits}, norm, loss, counts
 
     def train(self, x, adapter_ids, grad_d):
         """(d, gradients of experts [E][H][H] fp32, of the router's logits [T][E], choices) for grad_d bf16 [T][H]."""
@@ -191,6 +246,32 @@ def check(T=300, seed=0):
     s = torch.sigmoid(free).gather(1, ids.long())
     ((s / s.sum(1, keepdim=True)) * grad_weights.double()).sum().backward()
     out["gradient of the logits"] = relative(grad_logits, free.grad)
+    # the 4-bit weights, from what they stand for
+    few = dict(w, shared=quantise_fp4(w["shared"])[2], experts=quantise_fp4(w["experts"])[2])
+    t = min(T, 32)
+    y = x[:t].double() @ few["shared"].double().t()
+    for i in range(few["lora_a"].shape[0]):
+        on = adapter_ids[:t] == i
+        y[on] += x[:t][on].double() @ few["lora_a"][i].to(torch.bfloat16).double().t() @ \
+            few["lora_b"][i].to(torch.bfloat16).double().t()
+    _, ids4, weights4 = layer.route(y.to(torch.bfloat16))
+    out["served, 4-bit"] = relative(layer.serve_few(x[:t], adapter_ids[:t]),
+                                    reference(few, x[:t], adapter_ids[:t], ids4, weights4))
+    # the balance loss of sequences of a third and two thirds, by differentiation
+    starts = torch.tensor([0, T // 3, T], dtype=torch.int32, device="cuda")
+    _, grads, norm, loss, counts = layer.train_step(x, adapter_ids, grad_d, starts, balance=0.1, max_norm=1e9)
+    free = logits.double().requires_grad_(True)
+    p = torch.sigmoid(free)
+    p = p / p.sum(1, keepdim=True)
+    wanted = []
+    for a, b in ((0, T // 3), (T // 3, T)):
+        f = torch.bincount(ids[a:b].flatten(), minlength=E).double() * E / (layer.top_k * max(1, b - a))
+        wanted.append(0.1 * (f * p[a:b].sum(0)).sum() / max(1, b - a))
+    sum(wanted).backward()
+    out["balance loss"] = relative(loss, torch.stack(wanted).detach())
+    out["gradient with the balance loss"] = relative(grads["logits"], grad_logits.double() + free.grad)
+    out["norm"] = relative(norm, torch.sqrt(grads["experts"].double().square().sum() +
+                                            grads["logits"].double().square().sum()).view(1))
     return out
 
 

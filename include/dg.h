@@ -438,8 +438,8 @@ int dg_lora_bf16_nt(const void* x, int ldx, const void* a, const void* b, const 
  * finite value.  Sigmoids keep their shares however far below zero all of a
  * token's logits lie; shares below 2^-126 are 0.  E at most 1024, top_k at most
  * 64, T * top_k at most 2^30 (DG_ERR_UNSUPPORTED otherwise).  Scratch: workspace
- * (DG_ERR_UNSUPPORTED if a bound one has no room for 16 bytes per expert, E
- * rounded up to a multiple of 4).  Returns a dg_status. */
+ * (DG_ERR_UNSUPPORTED if a bound one has no room for 16 bytes per expert, their
+ * number rounded up to a multiple of 4).  Returns a dg_status. */
 int dg_route_balance(const void* logits, int logits_type, const int32_t* topk_ids, const int32_t* seq_starts,
                      float* loss, int32_t* counts, int T, int E, int top_k, int num_seqs, int score, float scale,
                      void* stream);
@@ -475,9 +475,9 @@ int dg_route_balance_backward(const void* logits, int logits_type, const int32_t
  *   c  bf16 [M] rows of N values, ldc apart, or NULL (0); may equal d
  *   d  bf16 [M] rows of N values, ldd apart
  * x is finite in the integer form (an infinity makes its token's results NaN).  K
- * must be a multiple of 128, N at most 2^20, odd ones too (DG_ERR_UNSUPPORTED
- * otherwise).  Any M, in tiles of 16 tokens that each read the weights: from a few
- * hundred tokens on the FP8 products take less time.  Returns a dg_status. */
+ * must be a multiple of 128 and at most 2^24, N at most 2^20, odd ones too
+ * (DG_ERR_UNSUPPORTED otherwise).  Any M, in tiles of 16 tokens that each read the
+ * weights: many tokens take less time in the FP8 products.  Returns a dg_status. */
 int dg_bf16_fp4_gemv_nt(const void* x, int ldx, const void* b, const int32_t* sfb, const void* c, int ldc, void* d,
                         int ldd, int M, int N, int K, void* stream);
 int dg_bf16_int4_gemv_nt(const void* x, int ldx, const void* b, const void* scales, int scales_type, const void* zeros,
@@ -494,7 +494,7 @@ int dg_bf16_int4_gemv_nt(const void* x, int ldx, const void* b, const void* scal
  *   c, d  rows of N values for T * top_k choices, as above
  * A choice whose expert is not here gets c (zeros without one), so that a gather
  * with row_of[t][j] = t * top_k + j sums what this GPU's experts give.  num_groups
- * at most 1024, T * top_k at most 2^30.  Scratch: workspace (lists, from 513
+ * at most 1024, T * top_k at most 2^30.  Scratch: workspace (lists, from 2049
  * choices on; a small one costs speed only).  Returns a dg_status. */
 int dg_m_grouped_bf16_fp4_gemv_nt_topk(const void* x, int ldx, int x_rows, const int32_t* topk_ids, const void* b,
                                        const int32_t* sfb, const void* c, int ldc, void* d, int ldd, int T, int top_k,
