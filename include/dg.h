@@ -461,8 +461,7 @@ int dg_route_balance_backward(const void* logits, int logits_type, const int32_t
  * for the tokens of a decoding step, where reading the weights is all the time.
  * The FP4 form takes the weights of dg_fp8_fp4_gemm_nt as they are stored:
  *   w[n][k] = e2m1(b[n][k]) * 2^(e[n][k/32] - 127), as a bf16 value: exact, but
- *           rounded to it below 2^-126, and an infinity from 2^128 on; a NaN
- *           where e = 255
+ *           an infinity from 2^128 on; a NaN where e = 255
  *   b uint8 [N][K/2] (16-byte aligned), sfb int32 [K/128][N] (4-byte aligned)
  * the integer form groups of group_size (32, 64 or 128) values along K:
  *   w[n][k] = (q[n][k] - zeros[k/group_size][n]) * scales[k/group_size][n]
@@ -470,7 +469,8 @@ int dg_route_balance_backward(const void* logits, int logits_type, const int32_t
  *           (16-byte aligned)
  *   scales scales_type [K/group_size][N]  DG_F32 or DG_BF16
  *   zeros uint8 [K/group_size][N] or NULL: 8
- * A group's sum of x * q and its sum of x are fp32 sums, joined and scaled in fp32.
+ * A group's sum of x * q and its sum of x are fp32 sums, scaled and joined in fp32
+ * (a scale times its zero point stays within fp32's range).
  *   x  bf16 [M] rows of K values, ldx apart (16-byte aligned, ldx % 8 == 0)
  *   c  bf16 [M] rows of N values, ldc apart, or NULL (0); may equal d
  *   d  bf16 [M] rows of N values, ldd apart

@@ -393,7 +393,7 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 def _run(fn, tensors, args, stream):
     """Checks that every tensor (None left out) lives on the current device, then makes the call.
     These calls take a few microseconds on the device, so the host side is kept as short."""
-    here = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    here = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
     for t in tensors.values():
         if t is not None and t.get_device() != here:
             _on_device(**tensors)
@@ -550,6 +550,8 @@ def _strided(t, name, shape, allow_none=False):
     """(address, row stride) of a bf16 matrix whose rows are contiguous and may lie apart (a column slice)."""
     if t is None and allow_none:
         return None, shape[1]
+    if type(t) is torch.Tensor and t.dtype is torch.bfloat16 and t.shape == shape and t.is_contiguous():
+        return t.data_ptr(), shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _BF16:
