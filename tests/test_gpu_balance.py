@@ -215,3 +215,46 @@ def test_the_same_bits_from_run_to_run(dg):
     _, x, ids, starts = problem(11, 5000, 160, 8, 3, "float32")
     a, b = (forward(dg, x, ids, starts, "sigmoid") for _ in range(2))
     assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+ORDER = [
+    # T, sequences: several per chunk of 64 tokens, one over many chunks, ends at the chunks' own ends
+    (640, [0, 64, 128, 640]), (640, [0, 1, 2, 3, 63, 64, 65, 127, 128, 129, 640]), (3000, [5, 5, 5, 1999, 2000, 2001, 2999]),
+    (4096, [0, 4096]), (4097, [0, 0, 4097, 4097]), (40000, [0, 13, 30000, 39999]),
+]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [60, 256, 400, 1000])
+@pytest.mark.parametrize("case", ORDER, ids=lambda c: f"{c[0]}-{len(c[1]) - 1}")
+def test_sequences_across_chunks(dg, case, E, score):
+    T, starts = case
+    print(f"case: balance of {T} tokens in {len(starts) - 1} sequences, {E} experts, {score}", flush=True)
+    T = T if E < 400 else min(T, 5000)
+    starts = np.minimum(starts, T).astype(np.int32)
+    _, x, ids, _ = problem(T + E, T, E, 5, 0, "bfloat16", masked=0.02)
+    loss, counts = forward(dg, x, ids, starts, score)
+    want, n = layer.balance(x.float().numpy(), ids, starts, score)
+    assert np.array_equal(counts, n)
+    # a lane adds up to T / 256 / 32 tokens by itself, 32 lanes' sums and then fp64
+    assert np.all(np.abs(loss - want) <= (E + 160 + T / 2048) * UNIT * want)
+    if T <= 4097:
+        out = torch.empty(T, E, dtype=torch.bfloat16, device="cuda")
+        dg.dg_route_balance_backward(x.cuda(), dev(counts), dev(starts), None, None, out, 5, score=score)
+        want, mag = layer.balance_backward(x.float().numpy(), counts, starts, None, None, 5, score)
+        got = out.double().cpu().numpy()
+        bound = HALF["bfloat16"] * np.abs(want) + (E + 33) * UNIT * mag + 1e-37
+        assert np.all(np.abs(got - want) <= bound), float((np.abs(got - want) / bound).max())
+
+
+def test_counts_of_other_gpus(dg):
+    """The gradient takes counts as they are given: those of a whole job's tokens, up to the ends of int32."""
+    T, E, k = 20, 16, 4
+    rng, x, ids, _ = problem(6, T, E, k, 0, "float32")
+    counts = rng.integers(0, 2 ** 31 - 1, (1, E)).astype(np.int32)
+    counts[0, :2] = 0, 2 ** 31 - 1
+    out = torch.empty(T, E, device="cuda")
+    for score in ("softmax", "sigmoid"):
+        dg.dg_route_balance_backward(x.cuda(), dev(counts), None, None, None, out, k, score=score)
+        want, mag = layer.balance_backward(x.numpy(), counts, None, None, None, k, score)
+        assert np.all(np.abs(out.double().cpu().numpy() - want) <= UNIT * np.abs(want) + (E + 33) * UNIT * mag)
