@@ -8,7 +8,6 @@ libdg.so behind the C ABI of include/dg.h; this package is its Python binding.""
 from ._lib import (  # noqa: F401
     DGError,
     EXPORTED,
-    GradList,
     LIB_PATH,
     dg_bf16_fp4_gemv_nt,
     dg_bf16_int4_gemv_nt,

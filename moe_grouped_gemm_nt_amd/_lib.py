@@ -1,11 +1,12 @@
-"""ctypes binding of libdg.so (the C ABI in include/dg.h).
+"""Binding of libdg.so (the C ABI in include/dg.h), by ctypes; for the calls that
+take a few microseconds with a native side (csrc/binding.cpp) that makes them
+where every argument is as it should be.
 
 Argument marshalling only: torch tensors in, device pointers and the current
 HIP stream out.  Every step of the computation runs in the library's kernels;
 there is no fallback path.  A missing library raises at first use."""
 from __future__ import annotations
 
-import array
 import ctypes
 import os
 import threading
@@ -406,6 +407,37 @@ def _run(fn, tensors, args, stream):
         _check(fn, status)
 
 
+_native = None
+
+
+def _load_native():
+    """The native side of the binding, with the addresses of the C calls; raises if it has not been built."""
+    global _native
+    lib = load()
+    with _lock:
+        if _native is None:
+            try:
+                from . import _binding
+            except ImportError as e:
+                raise RuntimeError("_binding.so is missing or does not fit this torch: build it with "
+                                   "`python -m moe_grouped_gemm_nt_amd.build`") from e
+            _binding.init({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in EXPORTED},
+                          torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+            _native = _binding
+    return _native
+
+
+def _fast(fn, *args):
+    """Makes the call through the native side of the binding and returns True; False where an argument is not exactly
+    what the call takes, for the checks below to name."""
+    status = getattr(_native or _load_native(), fn)(*args)
+    if status is None:
+        return False
+    if status:
+        _check(fn, status)
+    return True
+
+
 def _score(score):
     if score not in SCORES:
         raise ValueError(f"score is {score!r}; expected one of {sorted(SCORES)}")
@@ -589,6 +621,8 @@ def _starts(seq_starts, S):
 def dg_route_balance(logits, topk_ids, seq_starts, loss, counts, score="softmax", scale=1.0, stream=None) -> None:
     """The router's balance loss per sequence, loss fp32 [S], and the experts' counts, int32 [S][E], of
     logits [T][E] (fp32 or bf16) and topk_ids int32 [T][top_k]; seq_starts int32 [S + 1], or None for one sequence."""
+    if _fast("dg_route_balance", logits, topk_ids, seq_starts, loss, counts, _score(score), scale, stream):
+        return
     T, E = _rank(logits, "logits", (2,))
     k = _rank(topk_ids, "topk_ids", (2,))[1]
     S = _rank(loss, "loss", (1,))[0]
@@ -603,6 +637,9 @@ def dg_route_balance_backward(logits, counts, seq_starts, grad_loss, c, grad_log
                               stream=None) -> None:
     """grad_logits = c + the balance loss's gradient [T][E] (of the logits' type; c None: 0) for the forward call's
     counts [S][E] and grad_loss fp32 [S] (None: ones)."""
+    if _fast("dg_route_balance_backward", logits, counts, seq_starts, grad_loss, c, grad_logits, top_k, _score(score),
+             scale, stream):
+        return
     T, E = _rank(logits, "logits", (2,))
     S = _rank(counts, "counts", (2,))[0]
     args = (_ptr(logits, "logits", _LOGITS, None), 0 if logits.dtype == torch.float32 else 1,
@@ -633,6 +670,8 @@ def dg_bf16_fp4_gemv_nt(x, b, sfb, c, d, stream=None) -> None:
     """d[M][N] = bf16(c + x . dequant(b)^T) for a few tokens: x bf16 [M][K], b packed E2M1 [N][K/2], sfb int32
     [K/128][N] (as dg_fp8_fp4_gemm_nt takes them), c (or None) and d bf16 [M][N].  The rows of x, c and d may lie
     apart."""
+    if _fast("dg_bf16_fp4_gemv_nt", x, b, sfb, c, d, stream):
+        return
     M, K = _rank(x, "x", (2,))
     N = _rank(b, "b", (2,))[0]
     px, ldx = _strided(x, "x", (M, K))
@@ -645,6 +684,8 @@ def dg_bf16_fp4_gemv_nt(x, b, sfb, c, d, stream=None) -> None:
 def dg_bf16_int4_gemv_nt(x, b, scales, zeros, c, d, stream=None) -> None:
     """As dg_bf16_fp4_gemv_nt with integer weights: b [N][K/2] (two values of 0 to 15 per byte), scales fp32 or bf16
     [K/group][N] with groups of 32, 64 or 128 values, zeros uint8 [K/group][N] or None (8)."""
+    if _fast("dg_bf16_int4_gemv_nt", x, b, scales, zeros, c, d, stream):
+        return
     M, K = _rank(x, "x", (2,))
     N = _rank(b, "b", (2,))[0]
     px, ldx = _strided(x, "x", (M, K))
@@ -658,6 +699,8 @@ def dg_m_grouped_bf16_fp4_gemv_nt_topk(x, topk_ids, first_expert, b, sfb, c, d, 
     """The products of every choice with its expert's weights: topk_ids int32 [T][top_k], x bf16 [T][K] (a token's
     choices share its row) or [T * top_k][K], b [G][N][K/2], sfb int32 [G][K/128][N], c (or None) and d bf16
     [T * top_k][N]; a choice whose expert is not in [first_expert, first_expert + G) gets c, or zeros."""
+    if _fast("dg_m_grouped_bf16_fp4_gemv_nt_topk", x, topk_ids, first_expert, b, sfb, c, d, stream):
+        return
     T, k = _rank(topk_ids, "topk_ids", (2,))
     rows, K = _rank(x, "x", (2,))
     G, N, _ = _rank(b, "b", (3,))
@@ -672,6 +715,8 @@ def dg_m_grouped_bf16_fp4_gemv_nt_topk(x, topk_ids, first_expert, b, sfb, c, d, 
 def dg_m_grouped_bf16_int4_gemv_nt_topk(x, topk_ids, first_expert, b, scales, zeros, c, d, stream=None) -> None:
     """As dg_m_grouped_bf16_fp4_gemv_nt_topk with integer weights: b [G][N][K/2], scales fp32 or bf16 [G][K/group][N],
     zeros uint8 [G][K/group][N] or None (8)."""
+    if _fast("dg_m_grouped_bf16_int4_gemv_nt_topk", x, topk_ids, first_expert, b, scales, zeros, c, d, stream):
+        return
     T, k = _rank(topk_ids, "topk_ids", (2,))
     rows, K = _rank(x, "x", (2,))
     G, N, _ = _rank(b, "b", (3,))
@@ -684,63 +729,36 @@ def dg_m_grouped_bf16_int4_gemv_nt_topk(x, topk_ids, first_expert, b, scales, ze
                                                      d=d), args, stream)
 
 
-_GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}
-
-
 def _grad_arrays(tensors):
-    """(addresses, types, sizes) of fp32 and bf16 tensors that are contiguous and on the current device, as arrays
-    whose buffers the library reads during the call.  One pass per property: a loop over hundreds of small tensors
-    would take longer than the kernels."""
-    T = torch.Tensor
-    try:
-        types = array.array("i", [_GRAD_TYPES[t.dtype] for t in tensors])
-        fine = all(map(T.is_contiguous, tensors)) and len(set(map(T.get_device, tensors))) <= 1
-    except (TypeError, KeyError, AttributeError):
-        fine = False
-    if not fine:
-        for i, t in enumerate(tensors):
-            _ptr(t, f"tensor {i}", _LOGITS, None)
+    """(addresses, types, sizes) of fp32 and bf16 tensors, contiguous and on one device, as the library reads them."""
+    n = len(tensors)
+    pointers = (ctypes.c_void_p * n)(*[_ptr(t, f"tensor {i}", _LOGITS, None) for i, t in enumerate(tensors)])
+    if len({t.get_device() for t in tensors}) > 1:
         raise ValueError("the tensors must be on one device")
-    return array.array("Q", map(T.data_ptr, tensors)), types, array.array("q", map(T.numel, tensors))
-
-
-class GradList:
-    """Tensors (fp32 or bf16, contiguous, on one device) as the gradient calls take them, prepared once for gradients
-    that stay where they are: the list keeps their memory, not the tensor objects, and speaks of it whatever these
-    become later."""
-
-    def __init__(self, tensors):
-        tensors = list(tensors)
-        self.arrays = _grad_arrays(tensors)
-        self.tensors = [t.detach() for t in tensors]
-
-    def __len__(self):
-        return len(self.tensors)
-
-
-def _grads(tensors):
-    """(arrays, one of the tensors or None) of a GradList or a sequence of tensors"""
-    if isinstance(tensors, GradList):
-        return tensors.arrays, tensors.tensors[0] if tensors.tensors else None
-    if not isinstance(tensors, (list, tuple)):
-        tensors = list(tensors)
-    return _grad_arrays(tensors), tensors[0] if tensors else None
+    return (pointers, (ctypes.c_int * n)(*[0 if t.dtype == torch.float32 else 1 for t in tensors]),
+            (ctypes.c_longlong * n)(*[t.numel() for t in tensors]))
 
 
 def dg_grad_norm(grads, norm, stream=None) -> None:
-    """norm fp32 [1] = the 2-norm of all tensors together: a sequence of fp32 and bf16 tensors, or a GradList."""
-    (pointers, types, sizes), one = _grads(grads)
-    args = (pointers.buffer_info()[0], types.buffer_info()[0], sizes.buffer_info()[0], len(types),
-            _ptr(norm, "norm", _F32, (1,)))
-    _run("dg_grad_norm", dict(grads=one, norm=norm), args, stream)
+    """norm fp32 [1] = the 2-norm of all tensors of the list together (fp32 and bf16 ones)."""
+    grads = grads if isinstance(grads, (list, tuple)) else list(grads)
+    if _fast("dg_grad_norm", grads, norm, stream):
+        return
+    pointers, types, sizes = _grad_arrays(grads)
+    args = (pointers, types, sizes, len(grads), _ptr(norm, "norm", _F32, (1,)))
+    _run("dg_grad_norm", dict(grads=grads[0] if grads else None, norm=norm), args, stream)
 
 
 def dg_grad_clip(grads, out, norm, max_norm, stream=None) -> None:
     """out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), of the same types and sizes; out may be grads."""
-    (pointers, types, sizes), one = _grads(grads)
-    (out_pointers, out_types, out_sizes), two = (((pointers, types, sizes), one) if out is grads else _grads(out))
-    if types != out_types or sizes != out_sizes:
+    same = out is grads
+    grads = grads if isinstance(grads, (list, tuple)) else list(grads)
+    out = grads if same else out if isinstance(out, (list, tuple)) else list(out)
+    if _fast("dg_grad_clip", grads, out, norm, max_norm, stream):
+        return
+    pointers, types, sizes = _grad_arrays(grads)
+    out_pointers, out_types, out_sizes = _grad_arrays(out)
+    if types[:] != out_types[:] or sizes[:] != out_sizes[:]:
         raise ValueError("out must have the types and sizes of grads")
-    args = (pointers.buffer_info()[0], out_pointers.buffer_info()[0], types.buffer_info()[0], sizes.buffer_info()[0],
-            len(types), _ptr(norm, "norm", _F32, (1,)), float(max_norm))
-    _run("dg_grad_clip", dict(grads=one, out=two, norm=norm), args, stream)
+    args = (pointers, out_pointers, types, sizes, len(grads), _ptr(norm, "norm", _F32, (1,)), float(max_norm))
+    _run("dg_grad_clip", dict(grads=grads[0] if grads else None, out=out[0] if out else None, norm=norm), args, stream)

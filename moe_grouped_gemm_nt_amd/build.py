@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +17,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libdg.so")
 CEILINGS_PATH = os.path.join(PKG_DIR, "libdg_ceilings.so")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 # source -> extra flags.  The fp32-promotion kernels want MFMA results in
 # VGPRs, where the promotion FMAs read them; the power-of-two-scale kernels
 # keep their accumulators in AGPRs.
@@ -55,7 +57,7 @@ def _run(cmd, verbose):
     # the host pass does not know the packed-fp32 feature flag; that warning is expected
     lines = [l for l in out.splitlines() if "packed-fp32-ops" not in l and l.strip()]
     if r.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(lines))
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + "\n".join(lines))
     if verbose and lines:
         print("\n".join(lines))
 
@@ -69,14 +71,34 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         jobs.append(([hipcc()] + HIPCC_FLAGS + flags + list(extra_flags or []) +
                      ["-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", obj], obj))
     # the sources compile independently; one process each
-    with ThreadPoolExecutor(max_workers=min(len(jobs), 8)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, 8)) as ex:
+        binding = ex.submit(build_binding, verbose)
         list(ex.map(lambda j: _run(j[0], verbose), jobs))
+        binding.result()
     objs = [obj for _, obj in jobs]
     tmp = LIB_PATH + ".tmp"
     _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs, verbose)
     os.replace(tmp, LIB_PATH)
     build_ceilings(verbose)
     return LIB_PATH
+
+
+def build_binding(verbose: bool = False) -> str:
+    """_binding.so: the native side of the Python binding (host code only, against torch's libraries)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found; it is required to build _binding.so")
+    tmp = BINDING_PATH + ".tmp"
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-isystem", os.path.join(root, "include"),
+          "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+          "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"], verbose)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
 
 
 def build_ceilings(verbose: bool = False) -> str:

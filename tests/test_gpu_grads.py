@@ -120,19 +120,21 @@ def test_no_tensors(dg):
     assert float(norm_of(dg, [empty])) == 0.0
 
 
-def test_a_prepared_list(dg):
+def test_lists_of_all_kinds(dg):
+    """Tuples, generators, parameters and views, through both sides of the binding, give the same bits."""
     grads = tensors(3, [100, 7, 5000], [F, H])
-    lists = dg.GradList(grads)
-    a, b = norm_of(dg, lists), norm_of(dg, grads)
-    assert torch.equal(a, b)
-    want = [g.double() * layer.grad_factor(float(a), 1.0) for g in grads]
-    dg.dg_grad_clip(lists, lists, a, 1.0)
-    for g, w in zip(grads, want):
-        assert ((g.double() - w).abs() <= (HALF[g.dtype] + 3 * UNIT) * w.abs()).all()
-    # the list's memory is that of the tensors as they were
-    held = lists.tensors[0]
-    grads[0].data = torch.zeros(3, device="cuda")
-    assert held.numel() == 100
+    want = norm_of(dg, grads)
+    for same in (tuple(grads), iter(grads), [torch.nn.Parameter(g) for g in grads], [g.view(-1, 1) for g in grads]):
+        assert torch.equal(norm_of(dg, same), want)
+    other = torch.cuda.Stream()                  # (a stream object takes the checks in Python)
+    other.wait_stream(torch.cuda.current_stream())
+    norm, outs = torch.empty(1, device="cuda"), [torch.empty_like(g) for g in grads]
+    dg.dg_grad_norm(grads, norm, stream=other)
+    dg.dg_grad_clip(grads, outs, norm, 1.0, stream=other)
+    other.synchronize()
+    assert torch.equal(norm, want)
+    dg.dg_grad_clip(iter(grads), tuple(grads), want, 1.0)
+    assert all(torch.equal(g, o) for g, o in zip(grads, outs))
 
 
 def test_small_workspace_and_the_same_bits(dg):
