@@ -5,6 +5,7 @@
 //   r_i = 1 (softmax) or sigmoid(-x_i)
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 
 #include "../../include/dg.h"
@@ -20,7 +21,8 @@ constexpr long long kMaxChoices = 1LL << 30;
 constexpr int THREADS = 256;
 // 256 threads per chunk make twice the sums for the second kernel (one sequence of
 // 16384 tokens of 256 experts 21.9 us against 17.7, 131072 tokens of 128 experts in
-// 16 sequences 30 against 22), 1024 hold more tokens back behind a barrier (17.0 and 24).
+// 16 sequences 30 against 22), 1024 hold more tokens back behind a barrier (17.0 and 24;
+// all of them with a slower second kernel: 512 now take 15.5 in the first case).
 constexpr int kSumThreads = 512;
 constexpr long long kSequencesPerLaunch = 1 << 20;               // workgroups of up to 1024 threads: a grid has 2^32
 
@@ -316,13 +318,28 @@ __global__ __launch_bounds__(N) void balance_loss_kernel(BalanceParams p) {
     lds_sum[threadIdx.x][i] = sum[i];
     lds_count[threadIdx.x][i] = count[i];
   }
+  // by halves down to eight rows: few experts leave many (8 of them 512, which a thread
+  // each would take 13 us to add up)
+  int left = rows;
+  while (left > 8) {
+    const int half = (left + 1) / 2;
+    __syncthreads();
+    if (r + half < left) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lds_sum[threadIdx.x][i] += lds_sum[threadIdx.x + half * quads][i];
+        lds_count[threadIdx.x][i] += lds_count[threadIdx.x + half * quads][i];
+      }
+    }
+    left = half;
+  }
   __syncthreads();
   double total = 0.0;
   for (int e = threadIdx.x; e < p.E; e += N) {
     double v = 0.0;
     int k = 0;
 #pragma unroll 4
-    for (int j = 0; j < rows; ++j) {
+    for (int j = 0; j < left; ++j) {
       v += lds_sum[j * quads + e / 4][e % 4];
       k += lds_count[j * quads + e / 4][e % 4];
     }
@@ -338,7 +355,7 @@ constexpr int kOneThreads = 1024;
 template <int LPT, int NV, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(kOneThreads) void balance_one_kernel(BalanceParams p) {
   constexpr int ROWS = kOneThreads / LPT;
-  __shared__ f32x4 sums[ROWS][LPT * NV];
+  __shared__ f32x4 sums[kOneThreads / 64][LPT * NV];
   __shared__ int hist[kColumns<LPT, NV>];
   __shared__ double parts[kOneThreads / 64];
   const int lane = threadIdx.x % LPT, row = threadIdx.x / LPT;
@@ -370,14 +387,22 @@ __global__ __launch_bounds__(kOneThreads) void balance_one_kernel(BalanceParams 
       for (int v = 0; v < NV; ++v) acc[v] += x[h][v] * inv;
     }
   }
+  // a wave's rows are added in their registers, the waves' through shared memory
 #pragma unroll
-  for (int v = 0; v < NV; ++v) sums[row][v * LPT + lane] = acc[v];
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (LPT <= 32) acc[v][i] += __shfl_xor(acc[v][i], 32);
+      if constexpr (LPT <= 16) acc[v][i] += __shfl_xor(acc[v][i], 16);
+    }
+    if (threadIdx.x % 64 < LPT) sums[threadIdx.x / 64][v * LPT + lane] = acc[v];
+  }
   __syncthreads();
   double total = 0.0;
   for (int e = threadIdx.x; e < p.E; e += kOneThreads) {
     double sum = 0.0;
 #pragma unroll 8
-    for (int r = 0; r < ROWS; ++r) sum += reinterpret_cast<const float*>(&sums[r][0])[e];
+    for (int r = 0; r < kOneThreads / 64; ++r) sum += reinterpret_cast<const float*>(&sums[r][0])[e];
     p.counts[(size_t)s * p.E + e] = hist[e];
     total += sum * hist[e];
   }
@@ -536,14 +561,22 @@ void launch_kernel(const BalanceParams& p, bool bf, int score, int grid, hipStre
     launch_shape<WHICH, 64, 4>(p, bf, score, grid, st);
 }
 
-// One workgroup per sequence up to here, by all tokens' logits (one CU takes about
-// 0.25 ns for each): 512 tokens of 64 experts, called from Python, take 8.4 us against
-// 10.4 in two launches, 64 tokens of 256 replayed from a graph 5.9 against 8.7;
-// 1024 of 64 16 against 7.8.
-constexpr int kOneValues = 32768;
-// Tokens per chunk at the least: a block of the kernel of up to 256 experts.  One
-// sequence of 16384 tokens of 256 experts: 17.7 us, 25.6 with 32, 18.2 with 128.
-constexpr int kLeastChunk = 64;
+// One launch, with one workgroup per sequence, up to this many logits per sequence
+// (rows of fewer than 64 count as 64: they take the same lanes).  One CU takes about
+// 0.14 ns for each, two launches the more the wider their sums are.  From Python, one
+// launch and two: 64 tokens of 256 experts 5.2 us and 8.1, 128 of 256 6.8 and 8.3, 192
+// of 128 6.3 and 7.0, 256 of 128 7.2 and 7.3, 256 of 64 5.6 and 7.1, 384 of 64 6.7 and
+// 7.0, 512 of 64 7.8 and 6.9, 1024 of 16 14.1 and 8.0.
+int one_values(int E) { return E <= 128 ? 24576 : 32768; }
+// The starts are on the device: four sequences' share at the most for all tokens, which
+// could be one sequence's (1024 tokens of 64 in 8 sequences 4.6 us and 7.5, in one of
+// them 13 and 7).
+constexpr int kOneShares = 4;
+
+// Tokens per chunk at the least: a block of the kernel.  One sequence of 16384 tokens
+// of 256 experts: 17.7 us with 64, 25.6 with 32, 18.2 with 128 (with a slower second
+// kernel than now); 64 tokens of 1024 10.3 with 16, 17.2 with 64.
+int least_chunk(int E) { return E <= 256 ? 64 : E <= 512 ? 32 : 16; }
 
 // Tokens per workgroup: a multiple of 16, at most `most` workgroups
 int chunk_for(int T, int most, int least) {
@@ -606,7 +639,8 @@ extern "C" int dg_route_balance(const void* logits, int logits_type, const int32
   p.S = num_seqs;
   p.row = (E + 3) / 4 * 4;
   p.scale = scale;
-  if ((long long)T * p.row <= kOneValues && num_seqs <= kSequencesPerLaunch) {
+  if ((long long)T * std::max(p.row, 64) <= (long long)one_values(E) * std::min(num_seqs, kOneShares) &&
+      num_seqs <= kSequencesPerLaunch) {
     launch_kernel<kOne>(p, logits_type == DG_BF16, score, num_seqs, st);
     return launched();
   }
@@ -619,7 +653,7 @@ extern "C" int dg_route_balance(const void* logits, int logits_type, const int32
   // half of the room at most for the chunks, two workgroups per CU where that is enough
   const size_t slots = sc.bytes / slot;
   const int most = (size_t)(2 * sc.num_cus) > slots / 2 ? (int)(slots / 2) : 2 * sc.num_cus;
-  p.chunk = chunk_for(T, most, kLeastChunk);
+  p.chunk = chunk_for(T, most, least_chunk(E));
   const int chunks = T > 0 ? (T - 1) / p.chunk + 1 : 0;
   // as many sequences at a time as there is room for, usually all
   size_t per = slots - chunks;
