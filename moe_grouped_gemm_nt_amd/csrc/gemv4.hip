@@ -11,8 +11,8 @@
 namespace dg {
 namespace {
 
-// Up to here every workgroup finds its tile's choices itself; beyond, layout kernels
-// make lists.
+// Up to here every workgroup finds its tile's choices itself, in eight loads per thread
+// (256 threads) at the most; beyond, layout kernels make lists, in launches of their own.
 constexpr int kInlineChoices = 2048;
 
 struct GemvParams {
@@ -197,9 +197,16 @@ __device__ __forceinline__ bf16x8 even_first(u32x4 x) {
 }
 
 // ---- the kernel ----------------------------------------------------------------
-// A workgroup has 16 * RT columns of d, as the MFMA's rows, for one tile of choices,
-// the MFMA's columns; its W waves take pieces of 256 K in turn, each with LDS of its
-// own (no barrier until the sums are joined).  Bound by reading the weights.
+// A workgroup has 16 * RT columns of d, as the MFMA's columns, for one tile of choices,
+// the MFMA's rows; its W waves take pieces of 256 K in turn, each with LDS of its own
+// (no barrier until the sums are joined).
+//
+// Bound by reading the weights where these are many: one token of 65536 x 7168 takes
+// 36.7 us (6.8 TB/s of FP4; a device copy reaches 5.1), four of int4 43 (5.7 TB/s);
+// 64 tokens of 8 of 128 experts, 32 of them here, of 4096 x 7168 96 (5.2 TB/s).
+// 2112 x 7168 of one token is a launch and a chain of four loads: 5.9 us replayed from
+// a graph, in which an empty kernel takes 2.3.  Integers run 10% behind E2M1: their
+// scales pass through registers, so that one piece is under way at a time, not three.
 //
 // A piece's rows of weights (one 128-byte line each) and of x come into LDS with
 // direct loads of whole lines, as many pieces at a time as there is room for, and
@@ -492,9 +499,10 @@ int launch_items(GemvParams p, int group, long long tiles, hipStream_t st) {
       const int grid = (p.items + 7) / 8 * 8;
       if (group == 0)
         gemv_kernel<0, RT, W, TILE, NS><<<grid, W * 64, 0, st>>>(p);
-      else if (group == 32)
-        gemv_kernel<32, (RT == 4 && W == 8 ? 2 : RT), W, TILE, NS><<<grid, W * 64, 0, st>>>(p);
-      else if (group == 64)
+      else if (group == 32) {
+        if constexpr (RT * W < 32)                               // (launch_tile asks for no more: LDS has no room)
+          gemv_kernel<32, RT, W, TILE, NS><<<grid, W * 64, 0, st>>>(p);
+      } else if (group == 64)
         gemv_kernel<64, RT, W, TILE, NS><<<grid, W * 64, 0, st>>>(p);
       else
         gemv_kernel<128, RT, W, TILE, NS><<<grid, W * 64, 0, st>>>(p);
@@ -505,8 +513,23 @@ int launch_items(GemvParams p, int group, long long tiles, hipStream_t st) {
   return DG_OK;
 }
 
-// Columns per workgroup (16 * RT), its waves W and the pieces NS that a wave has room
-// for, by how many workgroups per CU there would be.
+// Columns per workgroup (16 * RT), its waves W and the pieces NS that a full tile's wave
+// has room for: the widest with which there is more than one workgroup per CU.  Fewer
+// leave CUs idle, more read x (and the choices) again for fewer columns.  Measured, as
+// us of RT, W, NS (replayed from a graph, FP4 unless said):
+//   tiles of 16   64 tokens of 4096 x 7168    4,8,1 12.2   2,4,1 15.5   4,4,1 16.8
+//                 128 tokens of the same      4,4,1 16.6   4,8,1 18.5
+//                 16 of 65536 x 7168          4,4,1 50     4,8,1 53     2,4,1 59
+//                 16 of 7168 x 16384          2,8,1 19.5   4,8,1 23.7   1,8,1 27.4
+//                 16 of 2112 x 7168           1,8,1 8.8    2,8,1 9.7
+//   tiles of 4    one of 2112 x 7168          1,8,2 6.0    2,8,2 7.0    2,4,1 10.3
+//                 one of 7168 x 16384         2,8,2 13.8   1,8,2 14.1   2,4,1 20.5
+//                 the same of int4            2,8,2 15.6   1,8,2 18.3   2,4,1 28.4
+//                 one of 65536 x 7168         2,4,2 36.6   2,4,1 39.3   2,8,2 49.4
+// With K up to 4096 a wave of four has at most four pieces, and room for more only
+// costs occupancy: one token of 57344 x 2048 of int4 2,4,1 17.4, 2,4,2 18.6, the 8
+// experts of one token 18.8 and 20.9; so it does for tiles of 8 (8 tokens of 64
+// experts of 2048 x 4096 31.7 and 36.9).
 template <int TILE>
 int launch_tile(const GemvParams& p, int group, long long tiles, int num_cus, hipStream_t st) {
   auto full = [&](int rt) { return tiles * ((p.N + 16 * rt - 1) / (16 * rt)) > num_cus; };
@@ -526,7 +549,8 @@ int launch_tile(const GemvParams& p, int group, long long tiles, int num_cus, hi
 }
 
 // Tokens per tile: those of a small batch (an expert has no more of them, unless a
-// token's choices repeat it), which need less LDS for x
+// token's choices repeat it).  Tiles of 4 and 8 take 2 and 4 KB of LDS for x per piece
+// against 8: one token of 7168 x 16384 13.8 us, in the tile of 16's best form 19.5.
 int tile_of(int tokens) { return tokens <= 4 ? 4 : (tokens <= 8 ? 8 : 16); }
 
 int launch_tiles(const GemvParams& p, int group, int tile, long long tiles, int num_cus, hipStream_t st) {
@@ -623,6 +647,10 @@ int dense(GemvParams& p, int group, int M, const void* scales, size_t scale_size
   const int e = call_scratch(st, &sc);
   if (e != DG_OK) return e;
   const int tile = tile_of(M);
+  // more tiles than one read the weights again, from the caches if the first leaves them
+  // there: 64 tokens of 4096 x 7168 11.2 us against 12.2 with streaming loads, 128 16.6
+  // against 18.5.  An expert's tiles are few: streaming there, 98.8 us against 106 (64
+  // tokens, 32 experts here).
   p.again = M > tile;
   return launch_tiles(p, group, tile, ((long long)M + tile - 1) / tile, sc.num_cus, st);
 }
