@@ -494,7 +494,7 @@ int dg_bf16_int4_gemv_nt(const void* x, int ldx, const void* b, const void* scal
  *   c, d  rows of N values for T * top_k choices, as above
  * A choice whose expert is not here gets c (zeros without one), so that a gather
  * with row_of[t][j] = t * top_k + j sums what this GPU's experts give.  num_groups
- * at most 1024, T * top_k at most 2^30.  Scratch: workspace (lists, from 2049
+ * at most 1024, T * top_k at most 2^30.  Scratch: workspace (lists, from 1025
  * choices on; a small one costs speed only).  Returns a dg_status. */
 int dg_m_grouped_bf16_fp4_gemv_nt_topk(const void* x, int ldx, int x_rows, const int32_t* topk_ids, const void* b,
                                        const int32_t* sfb, const void* c, int ldc, void* d, int ldd, int T, int top_k,

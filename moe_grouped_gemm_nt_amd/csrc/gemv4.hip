@@ -11,9 +11,12 @@
 namespace dg {
 namespace {
 
-// Up to here every workgroup finds its tile's choices itself, in eight loads per thread
-// (256 threads) at the most; beyond, layout kernels make lists, in launches of their own.
-constexpr int kInlineChoices = 2048;
+// Up to here every workgroup finds its tile's choices itself, in four loads per thread
+// at the most; beyond, layout kernels make lists, in launches of their own.  Inline and
+// with lists, replayed from a graph: 64 tokens of 8 of 128 experts of 512 x 1024 14 us
+// and 19, 128 15.0 and 19.5, 256 22.6 and 23.7, of 4096 x 7168 with 32 experts here 64
+// tokens 95.1 and 96.8, 128 113 and 111, 256 174 and 166.
+constexpr int kInlineChoices = 1024;
 
 struct GemvParams {
   const uint16_t* x;
@@ -70,7 +73,7 @@ __device__ __forceinline__ int wave_scan(int v) {                // sums over th
 // the tiles are numbered by expert without gaps and few workgroups find none.  An
 // expert's only tile takes its choices in whatever order they were counted (no
 // result depends on a choice's place in its tile), one of several its sixteen in
-// the order of the choices.
+// the order of the choices, which all of its workgroups find alike.
 template <int THREADS, int TILE>
 __device__ __forceinline__ bool find_tile(const GemvParams& p, int tile, int* rows, int* id, int* room) {
   if (!p.ids) {
@@ -100,7 +103,7 @@ __device__ __forceinline__ bool find_tile(const GemvParams& p, int tile, int* ro
 #pragma unroll
     for (int j = 0; j < MOST; ++j) {
       if (j * THREADS >= p.n) break;
-      e[j] = local_expert(p, e[j]);
+      e[j] = local_expert(p, e[j]);                              // (-1 stays it: first >= 0)
       if (e[j] >= 0) place[j] = atomicAdd(&count[e[j]], 1);
     }
     __syncthreads();
@@ -125,14 +128,23 @@ __device__ __forceinline__ bool find_tile(const GemvParams& p, int tile, int* ro
         if (j * THREADS >= p.n) break;
         if (e[j] == mine) rows[place[j]] = p.i0 + (int)threadIdx.x + j * THREADS;
       }
-    } else if (threadIdx.x < 64) {
-      int seen = -at * TILE;
-      for (int base = 0; base < p.n && seen < TILE; base += 64) {
-        const bool is = base + lane < p.n && local_expert(p, p.ids[base + lane]) == mine;
-        const uint64_t m = __ballot(is);
-        const int to = seen + __popcll(m & ((1ull << lane) - 1));
-        if (is && to >= 0 && to < TILE) rows[to] = p.i0 + base + lane;
-        seen += __popcll(m);
+    } else {
+      // several tiles: in the order of the choices, by the numbers before each 64
+      constexpr int WAVES = THREADS / 64;
+      int* per = room + kMaxLayoutGroups;                        // [MOST * WAVES]
+      const int wave = threadIdx.x / 64;
+      uint64_t m[MOST];
+#pragma unroll
+      for (int j = 0; j < MOST; ++j) {
+        m[j] = __ballot(e[j] == mine);
+        if (lane == 0) per[j * WAVES + wave] = __popcll(m[j]);
+      }
+      __syncthreads();
+      const int v = lane < MOST * WAVES ? per[lane] : 0, upto = wave_scan(v);
+#pragma unroll
+      for (int j = 0; j < MOST; ++j) {
+        const int to = __shfl(upto - v, j * WAVES + wave) + __popcll(m[j] & ((1ull << lane) - 1)) - at * TILE;
+        if (e[j] == mine && to >= 0 && to < TILE) rows[to] = p.i0 + (int)threadIdx.x + j * THREADS;
       }
     }
   }
@@ -409,7 +421,7 @@ __global__ __launch_bounds__(W * 64) void gemv_kernel(GemvParams p) {
   constexpr int BW = kWaveBytes<FORM, RT, TILE, NS>;
   __shared__ int rows[16];
   __shared__ __attribute__((aligned(128))) uint8_t lds[W][BW];
-  static_assert(sizeof(lds) >= kMaxLayoutGroups * 4, "find_tile's room");
+  static_assert(sizeof(lds) >= (kMaxLayoutGroups + kInlineChoices / 64) * 4 && kInlineChoices <= 64 * 64, "find_tile's room");
   // consecutive workgroups go to the 8 XCDs in turn: each takes a run of items, the
   // tiles of the same columns next to one another, for those that share an expert
   const int per = (p.items + 7) / 8;
@@ -575,6 +587,11 @@ int launch_choices(GemvParams p, int group, int tile, int n, const int32_t* ids,
     }
     p.i0 = i;
     p.n = step;
+    // experts with several tiles each, as for the dense product (256 tokens of 2 of 8
+    // experts of 14336 x 4096 190 us against 200 with streaming loads, 512 of 8 of 128, 32
+    // here, of 4096 x 7168 224 against 247); with about one tile each streaming is better
+    // (64 and 128 tokens of the same 95 us against 103, 111 against 115)
+    p.again = step > 2LL * tile * p.G;
     p.ids = ids + i;
     p.layout = nullptr;
     p.slot_of = nullptr;
@@ -649,8 +666,7 @@ int dense(GemvParams& p, int group, int M, const void* scales, size_t scale_size
   const int tile = tile_of(M);
   // more tiles than one read the weights again, from the caches if the first leaves them
   // there: 64 tokens of 4096 x 7168 11.2 us against 12.2 with streaming loads, 128 16.6
-  // against 18.5.  An expert's tiles are few: streaming there, 98.8 us against 106 (64
-  // tokens, 32 experts here).
+  // against 18.5
   p.again = M > tile;
   return launch_tiles(p, group, tile, ((long long)M + tile - 1) / tile, sc.num_cus, st);
 }

@@ -114,3 +114,30 @@ def test_rows_that_repeat_are_the_same_bits(dg):
         for e in (0, 1):
             rows = d[(ids == e).view(-1)]
             assert bool((rows == rows[0]).all())
+
+
+@pytest.mark.parametrize("n", [1, 17, 63, 64, 65, 511, 1023, 1024, 1025, 2047, 2048, 2049])
+@pytest.mark.parametrize("G", [1, 3, 1024])
+def test_choices_around_the_lists(dg, n, G):
+    """One choice per token, with several tiles per expert, ids counted by every workgroup or listed."""
+    print(f"case: gemv of {n} choices of {G} experts", flush=True)
+    rng = np.random.default_rng(n + G)
+    N, K = 20, 128
+    args, w, most = weights(rng, "fp4", (G,), N, K)
+    ids = rng.integers(-1, G + 1, (n, 1)).astype(np.int32)
+    x = bf16(rng, n, K)
+    d = torch.full((n, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_m_grouped_bf16_fp4_gemv_nt_topk(x.cuda(), dev(ids), 0, *args, None, d)
+    torch.cuda.synchronize()
+    flat, xd = ids.ravel(), x.double()
+    here = (flat >= 0) & (flat < G)
+    wd, md = torch.from_numpy(np.asarray(w, dtype=np.float64)), torch.from_numpy(np.asarray(most, dtype=np.float64))
+    at = torch.from_numpy(np.clip(flat, 0, G - 1).astype(np.int64))
+    ref = torch.empty(n, N, dtype=torch.float64)
+    mag = torch.empty(n, N, dtype=torch.float64)
+    for i in range(n):
+        ref[i], mag[i] = wd[at[i]] @ xd[i], md[at[i]] @ xd[i].abs()
+    keep = torch.from_numpy(here)[:, None]
+    ref, mag = ref * keep, mag * keep
+    bound = 2.0 ** -8 * ref.abs() + (K + K // 16 + 16) * 2.0 ** -23 * mag + 1e-37
+    assert bool(((d.cpu().double() - ref).abs() <= bound).all())
