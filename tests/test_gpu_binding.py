@@ -89,3 +89,59 @@ def test_refusals_of_the_library_are_raised(dg):
     g = torch.zeros(64, device="cuda")
     with pytest.raises(dg.DGError, match="apart"):
         dg.dg_grad_clip([g[:32]], [g[16:48]], loss, 1.0)
+
+
+def test_two_host_threads(dg):
+    """Calls from two threads, each on its own stream with its own workspace, give the bits of calls in turn."""
+    import threading
+    results, errors = [None, None], []
+
+    def work(t):
+        try:
+            stream = torch.cuda.Stream()
+            ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+            with torch.cuda.stream(stream):
+                dg.dg_bind_stream_workspace(stream, ws)
+                try:
+                    made = [calls(dg, t)[name] for name in calls(dg, t)]
+                    for call, _ in made * 20:
+                        call()
+                    results[t] = [o.clone() for _, outputs in made for o in outputs]
+                    stream.synchronize()
+                finally:
+                    dg.dg_bind_stream_workspace(stream, None)
+        except Exception as e:                                    # (shown by the assertion below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for t in (0, 1):
+        made = [calls(dg, t)[name] for name in calls(dg, t)]
+        for call, _ in made * 20:
+            call()
+        want = [o for _, outputs in made for o in outputs]
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(results[t], want))
+
+
+def test_captured_and_replayed(dg):
+    """The calls in one graph, with eager ones of the same buffers between the replays."""
+    made = [calls(dg, 2)[name] for name in calls(dg, 2)]
+    eager = [calls(dg, 2)[name] for name in calls(dg, 2)]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        for call, _ in made:
+            call()
+    for _ in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        for call, _ in eager:
+            call()
+        torch.cuda.synchronize()
+        for (_, a), (_, b) in zip(made, eager):
+            assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(a, b))
