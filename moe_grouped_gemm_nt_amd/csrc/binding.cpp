@@ -6,6 +6,7 @@
 // A call takes about 0.4 us here besides the launch, 3.5 in Python.
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <initializer_list>
 #include <vector>
@@ -154,9 +155,11 @@ PyObject* finish(const Args& a, F call) {
   return PyLong_FromLong(status);
 }
 
-// What torch throws (a tensor without memory) is for the checks in Python to name
+// What torch throws (a tensor without memory) is for the checks in Python to name; before
+// init() no call is made
 template <typename F>
 PyObject* guarded(F f) {
+  if (!g_device) Py_RETURN_NONE;
   try {
     return f();
   } catch (...) {
@@ -354,24 +357,36 @@ PyObject* grad_clip(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// init({name: address}, current device, current raw stream)
+// init({name: address}, current device, current raw stream): all of it, or nothing where
+// an argument does not fit
 PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 3 || !PyDict_Check(args[0])) {
     PyErr_SetString(PyExc_TypeError, "init(addresses, current_device, current_raw_stream)");
     return nullptr;
   }
+  uintptr_t fn[kFns];
   for (int i = 0; i < kFns; ++i) {
     PyObject* v = PyDict_GetItemString(args[0], kNames[i]);
-    g_fn[i] = v ? (uintptr_t)PyLong_AsUnsignedLongLong(v) : 0;
-    if (!g_fn[i]) {
-      if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "no address of %s", kNames[i]);
+    const unsigned long long at = v ? PyLong_AsUnsignedLongLong(v) : 0;
+    if (PyErr_Occurred()) return nullptr;
+    if (!at) {
+      PyErr_Format(PyExc_ValueError, "no address of %s", kNames[i]);
       return nullptr;
     }
+    fn[i] = (uintptr_t)at;
   }
+  if (!PyCallable_Check(args[1]) || !PyCallable_Check(args[2])) {
+    PyErr_SetString(PyExc_TypeError, "the queries of the device and of its stream must be callable");
+    return nullptr;
+  }
+  std::copy(fn, fn + kFns, g_fn);
   Py_INCREF(args[1]);
   Py_INCREF(args[2]);
+  PyObject *device = g_device, *stream = g_stream;
   g_device = args[1];
   g_stream = args[2];
+  Py_XDECREF(device);
+  Py_XDECREF(stream);
   Py_RETURN_NONE;
 }
 
