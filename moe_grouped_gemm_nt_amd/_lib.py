@@ -1,6 +1,6 @@
 """Binding of libdg.so (the C ABI in include/dg.h), by ctypes; for the calls that
-take a few microseconds with a native side (csrc/binding.cpp) that makes them
-where every argument is as it should be.
+take a few microseconds with a native side (csrc/binding.cpp, _binding.so) that makes
+them where it has been built and every argument is as it should be.
 
 Argument marshalling only: torch tensors in, device pointers and the current
 HIP stream out.  Every step of the computation runs in the library's kernels;
@@ -10,11 +10,13 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 
 import torch
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG_DIR, "libdg.so")
+BINDING_PATH = os.path.join(_PKG_DIR, "_binding.so")
 
 DG_OK = 0
 DG_ERR_INVALID_ARG = -1
@@ -407,11 +409,12 @@ def _run(fn, tensors, args, stream):
         _check(fn, status)
 
 
-_native = None
+_native = None                 # False: there is none
 
 
 def _load_native():
-    """The native side of the binding, with the addresses of the C calls; raises if it has not been built."""
+    """The native side of the binding, with the addresses of the C calls, or False where it has not been built (without
+    torch's headers or g++) or does not fit this torch: the calls then go through ctypes, 4 us longer."""
     global _native
     lib = load()
     with _lock:
@@ -419,18 +422,25 @@ def _load_native():
             try:
                 from . import _binding
             except ImportError as e:
-                raise RuntimeError("_binding.so is missing or does not fit this torch: build it with "
-                                   "`python -m moe_grouped_gemm_nt_amd.build`") from e
-            _binding.init({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in EXPORTED},
-                          torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
-            _native = _binding
+                if os.path.exists(BINDING_PATH):
+                    warnings.warn(f"{BINDING_PATH} cannot be loaded ({e}): calls go through ctypes", RuntimeWarning)
+                _native = False
+            else:
+                _binding.init({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in EXPORTED},
+                              torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+                _native = _binding
     return _native
 
 
 def _fast(fn, *args):
-    """Makes the call through the native side of the binding and returns True; False where an argument is not exactly
-    what the call takes, for the checks below to name."""
-    status = getattr(_native or _load_native(), fn)(*args)
+    """Makes the call through the native side of the binding and returns True; False where there is none, or where an
+    argument is not exactly what the call takes, for the checks below to name."""
+    native = _native
+    if native is None:
+        native = _load_native()
+    if native is False:
+        return False
+    status = getattr(native, fn)(*args)
     if status is None:
         return False
     if status:

@@ -1,4 +1,5 @@
-"""Builds the gfx950 HIP library (libdg.so) in-tree with hipcc.
+"""Builds the gfx950 HIP library (libdg.so) in-tree with hipcc, and the native side of
+the Python binding (_binding.so) with g++ where torch and both headers are there.
 
 Usage: python -m moe_grouped_gemm_nt_amd.build [--verbose]
 """
@@ -70,28 +71,52 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         obj = os.path.join(objdir, src.replace(".hip", ".o"))
         jobs.append(([hipcc()] + HIPCC_FLAGS + flags + list(extra_flags or []) +
                      ["-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", obj], obj))
+    lacks = binding_lacks()
+    if os.path.exists(BINDING_PATH):
+        os.remove(BINDING_PATH)                    # none of other sources stays beside the library
     # the sources compile independently; one process each
     with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, 8)) as ex:
-        binding = ex.submit(build_binding, verbose)
+        binding = None if lacks else ex.submit(build_binding, verbose)
         list(ex.map(lambda j: _run(j[0], verbose), jobs))
-        binding.result()
     objs = [obj for _, obj in jobs]
     tmp = LIB_PATH + ".tmp"
     _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs, verbose)
     os.replace(tmp, LIB_PATH)
     build_ceilings(verbose)
+    if lacks:
+        print(f"_binding.so is left out ({lacks}): the calls that it shortens go through ctypes", file=sys.stderr)
+    else:
+        binding.result()
     return LIB_PATH
+
+
+def _cxx():
+    return shutil.which("g++") or shutil.which("c++")
+
+
+def binding_lacks() -> str | None:
+    """What is missing for _binding.so; libdg.so needs none of it."""
+    try:
+        import torch
+    except ImportError:
+        return "torch is not installed"
+    if not os.path.exists(os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "autograd",
+                                       "python_variable.h")):
+        return "torch's headers are not installed"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers are not installed"
+    return None if _cxx() else "g++ not found"
 
 
 def build_binding(verbose: bool = False) -> str:
     """_binding.so: the native side of the Python binding (host code only, against torch's libraries)."""
+    lacks = binding_lacks()
+    if lacks:
+        raise RuntimeError(f"_binding.so cannot be built: {lacks}")
     import torch
     root = os.path.dirname(torch.__file__)
-    cxx = shutil.which("g++") or shutil.which("c++")
-    if cxx is None:
-        raise RuntimeError("g++ not found; it is required to build _binding.so")
     tmp = BINDING_PATH + ".tmp"
-    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    _run([_cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           "-isystem", os.path.join(root, "include"),
           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
