@@ -436,7 +436,11 @@ int dg_lora_bf16_nt(const void* x, int ldx, const void* a, const void* b, const 
  * A logit of -inf or NaN is a masked expert's: its share is 0.  A token of masked
  * experts only has no shares, but counts in n_s.  +inf counts as the largest
  * finite value.  Sigmoids keep their shares however far below zero all of a
- * token's logits lie; shares below 2^-126 are 0.  E at most 1024, top_k at most
+ * token's logits lie; shares below 2^-126 are 0.  Shares are fp32 and summed in
+ * fp32 over stretches of tokens, two per CU (a small bound workspace makes them
+ * longer), and those sums and the loss in fp64: with 256 CUs and the device's
+ * workspace a loss is off by less than (E + 160 + T / 4096) * 2^-24 of itself.  E
+ * at most 1024, top_k at most
  * 64, T * top_k at most 2^30 (DG_ERR_UNSUPPORTED otherwise).  Scratch: workspace
  * (DG_ERR_UNSUPPORTED if a bound one has no room for 16 bytes per expert, their
  * number rounded up to a multiple of 4).  Returns a dg_status. */
@@ -469,23 +473,26 @@ int dg_route_balance_backward(const void* logits, int logits_type, const int32_t
  *           (16-byte aligned)
  *   scales scales_type [K/group_size][N]  DG_F32 or DG_BF16
  *   zeros uint8 [K/group_size][N] or NULL: 8
- * A group's sum of x * q and its sum of x are fp32 sums, scaled and joined in fp32
- * (a scale times its zero point stays within fp32's range).
+ * A group's sum of x * q and its sum of x are fp32 sums, scaled and joined in fp32:
+ * both sums, and a scale times its zero point, have to stay within fp32's range
+ * (the sums do where x is below 2^117 in magnitude), and the result's error is
+ * measured by magnitudes of (q + zero) * scale * x.
  *   x  bf16 [M] rows of K values, ldx apart (16-byte aligned, ldx % 8 == 0)
  *   c  bf16 [M] rows of N values, ldc apart, or NULL (0); may equal d
  *   d  bf16 [M] rows of N values, ldd apart
  * x is finite in the integer form (an infinity makes its token's results NaN).  K
  * must be a multiple of 128 and at most 2^24, N at most 2^20, odd ones too
- * (DG_ERR_UNSUPPORTED otherwise).  Any M, in tiles of 16 tokens that each read the
- * weights: many tokens take less time in the FP8 products.  Returns a dg_status. */
+ * (DG_ERR_UNSUPPORTED otherwise).  Any M, in tiles of 4, 8 or 16 tokens (up to 4, up
+ * to 8 and more in all) that each read the weights: many tokens take less time in the
+ * FP8 products.  Returns a dg_status. */
 int dg_bf16_fp4_gemv_nt(const void* x, int ldx, const void* b, const int32_t* sfb, const void* c, int ldc, void* d,
                         int ldd, int M, int N, int K, void* stream);
 int dg_bf16_int4_gemv_nt(const void* x, int ldx, const void* b, const void* scales, int scales_type, const void* zeros,
                          int group_size, const void* c, int ldc, void* d, int ldd, int M, int N, int K, void* stream);
 
 /* The same with the experts of every choice, straight from the router's ids: no
- * layout, no rows moved, an expert's weights read once for its choices (16 at a
- * time).  Choice i = t * top_k + j of expert e = topk_ids[t][j], local expert
+ * layout, no rows moved, an expert's weights read once for its choices (4, 8 or 16
+ * at a time, by T as by M above).  Choice i = t * top_k + j of expert e = topk_ids[t][j], local expert
  * g = e - first_expert in [0, num_groups):
  *   d[i][n] = bf16_rne( c[i][n] + sum_k x[row][k] * w[g][n][k] )
  *   x  rows of K values as above: x_rows = T, a token's choices sharing row t, or
@@ -523,7 +530,8 @@ int dg_grad_norm(const void* const* grads, const int* types, const long long* si
 
 /* The gradients scaled so that their norm is at most max_norm:
  *   out[i][j] = grads[i][j] * f,   f = min(1, max_norm / (norm[0] + 1e-6))
- * f in fp32, one rounding to each tensor's type.  norm is read by the kernels only,
+ * f and the products in fp32, those of bf16 tensors rounded once more to bf16.  norm
+ * is read by the kernels only,
  * so that a job may sum the squares of several GPUs in between.  A NaN norm makes f
  * NaN, an infinite one 0.
  *   grads, types, sizes as above; out num_tensors addresses on the HOST: each may

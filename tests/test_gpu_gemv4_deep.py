@@ -115,3 +115,18 @@ def check_choices(dg, form, ids, G, N, K, per_choice, g, first=0):
         if len(at):
             want[at] = product(rows[at], decode(form, *of_expert(args, e)), c[at])
     same(d, want, (ids.shape, G, N, K, form))
+
+
+@pytest.mark.parametrize("form", FORMS[1:], ids=str)
+def test_integers_with_the_largest_x(dg, form):
+    """x up to 2^116 and scales as small: a group's sums reach 2^127, the results are those of the small numbers."""
+    g = generator(1)
+    M, N, K = 9, 40, 1152
+    b, s, z = weights(g, form, (), N, K)
+    x, c = whole(g, M, K), quarters(g, M, N)
+    x[3], x[4] = 2.0, -2.0                       # sums of one sign
+    want = product(x, decode(form, b, s, z), c)
+    d = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dense(dg, form)(x * 2.0 ** 115, b, s * 2.0 ** -115, z, c, d)
+    torch.cuda.synchronize()
+    same(d, want, form)
