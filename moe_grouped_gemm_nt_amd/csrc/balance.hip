@@ -19,10 +19,11 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr long long kMaxChoices = 1LL << 30;
 constexpr int THREADS = 256;
-// 256 threads per chunk make twice the sums for the second kernel (one sequence of
-// 16384 tokens of 256 experts 21.9 us against 17.7, 131072 tokens of 128 experts in
-// 16 sequences 30 against 22), 1024 hold more tokens back behind a barrier (17.0 and 24;
-// all of them with a slower second kernel: 512 now take 15.5 in the first case).
+// One sequence of 16384 tokens of 256 experts, 8 of them, and 131072 tokens of 128
+// experts in 16 sequences (sigmoids, replayed from a graph): 17.5, 13.5 and 24 us.  256
+// threads per chunk make twice the sums for the second kernel (20.3, 16.4 and 33; with
+// chunks of 32 tokens 24.1, 14.8 and 33), 1024 hold more tokens back behind a barrier
+// (20.0, 16.2 and 26.6; with chunks of 128 17.1, 15.3 and 26.6).
 constexpr int kSumThreads = 512;
 constexpr long long kSequencesPerLaunch = 1 << 20;               // workgroups of up to 1024 threads: a grid has 2^32
 
@@ -564,18 +565,19 @@ void launch_kernel(const BalanceParams& p, bool bf, int score, int grid, hipStre
 // One launch, with one workgroup per sequence, up to this many logits per sequence
 // (rows of fewer than 64 count as 64: they take the same lanes).  One CU takes about
 // 0.14 ns for each, two launches the more the wider their sums are.  From Python, one
-// launch and two: 64 tokens of 256 experts 5.2 us and 8.1, 128 of 256 6.8 and 8.3, 192
-// of 128 6.3 and 7.0, 256 of 128 7.2 and 7.3, 256 of 64 5.6 and 7.1, 384 of 64 6.7 and
-// 7.0, 512 of 64 7.8 and 6.9, 1024 of 16 14.1 and 8.0.
+// launch and two (softmax): 64 tokens of 256 experts 5.4 us and 8.1, 128 of 256 7.0 and
+// 8.4, 192 of 128 6.5 and 7.1, 256 of 128 7.3 and 7.3, 256 of 64 5.7 and 6.9, 384 of 64
+// 7.0 and 6.9, 512 of 64 8.2 and 6.9, 1024 of 16 14.2 and 8.1.  Sigmoids cost one launch
+// more than two (192 of 128 7.4 and 7.5, 384 of 64 8.0 and 7.2).
 int one_values(int E) { return E <= 128 ? 24576 : 32768; }
 // The starts are on the device: four sequences' share at the most for all tokens, which
-// could be one sequence's (1024 tokens of 64 in 8 sequences 4.6 us and 7.5, in one of
-// them 13 and 7).
+// could be one sequence's (1024 tokens of 64 in 8 sequences 4.8 us and 7.6, in one of
+// them 14 and 8).
 constexpr int kOneShares = 4;
 
-// Tokens per chunk at the least: a block of the kernel.  One sequence of 16384 tokens
-// of 256 experts: 17.7 us with 64, 25.6 with 32, 18.2 with 128 (with a slower second
-// kernel than now); 64 tokens of 1024 10.3 with 16, 17.2 with 64.
+// Tokens per chunk at the least: a block of the kernel.  16384 tokens of 256 experts in
+// one sequence and in 8: 17.3 and 13.5 us with 64, 25.9 and 16.6 with 32, 18.2 and 16.4
+// with 128; 64 tokens of 1024 10.4 with 16, 13.3 with 32, 19.6 with 64.
 int least_chunk(int E) { return E <= 256 ? 64 : E <= 512 ? 32 : 16; }
 
 // Tokens per workgroup: a multiple of 16, at most `most` workgroups

@@ -13,9 +13,10 @@ namespace {
 
 // Up to here every workgroup finds its tile's choices itself, in four loads per thread
 // at the most; beyond, layout kernels make lists, in launches of their own.  Inline and
-// with lists, replayed from a graph: 64 tokens of 8 of 128 experts of 512 x 1024 14 us
-// and 19, 128 15.0 and 19.5, 256 22.6 and 23.7, of 4096 x 7168 with 32 experts here 64
-// tokens 95.1 and 96.8, 128 113 and 111, 256 174 and 166.
+// with lists, replayed from a graph: 64 tokens of 8 of 128 experts of 512 x 1024 13.1 us
+// and 18.5, 128 14.7 and 19.3, of 4096 x 7168 with 32 experts here 64 tokens 92 and 94,
+// 128 111 and 110; with the limit raised to 2048 (eight loads) 256 tokens of the small
+// experts 23.3 and 24.1, of the large ones 151 and 145.
 constexpr int kInlineChoices = 1024;
 
 struct GemvParams {
@@ -214,11 +215,12 @@ __device__ __forceinline__ bf16x8 even_first(u32x4 x) {
 // (no barrier until the sums are joined).
 //
 // Bound by reading the weights where these are many: one token of 65536 x 7168 takes
-// 36.7 us (6.8 TB/s of FP4; a device copy reaches 5.1), four of int4 43 (5.7 TB/s);
-// 64 tokens of 8 of 128 experts, 32 of them here, of 4096 x 7168 96 (5.2 TB/s).
-// 2112 x 7168 of one token is a launch and a chain of four loads: 5.9 us replayed from
-// a graph, in which an empty kernel takes 2.3.  Integers run 10% behind E2M1: their
-// scales pass through registers, so that one piece is under way at a time, not three.
+// 36.7 us (6.8 TB/s of FP4; a device copy reaches 5.1), four of int4 45 (5.4 TB/s);
+// 64 tokens of 8 of 128 experts, 32 of them here, of 4096 x 7168 92 (5.1 TB/s).
+// 2112 x 7168 of one token is a launch and a chain of four loads: 6.0 us replayed from
+// a graph, in which an empty kernel takes 2.3.  Integers run 10 to 20% behind E2M1:
+// their scales pass through registers, so that one piece is under way at a time, not
+// three.
 //
 // A piece's rows of weights (one 128-byte line each) and of x come into LDS with
 // direct loads of whole lines, as many pieces at a time as there is room for, and
@@ -529,19 +531,20 @@ int launch_items(GemvParams p, int group, long long tiles, hipStream_t st) {
 // has room for: the widest with which there is more than one workgroup per CU.  Fewer
 // leave CUs idle, more read x (and the choices) again for fewer columns.  Measured, as
 // us of RT, W, NS (replayed from a graph, FP4 unless said):
-//   tiles of 16   64 tokens of 4096 x 7168    4,8,1 12.2   2,4,1 15.5   4,4,1 16.8
-//                 128 tokens of the same      4,4,1 16.6   4,8,1 18.5
-//                 16 of 65536 x 7168          4,4,1 50     4,8,1 53     2,4,1 59
-//                 16 of 7168 x 16384          2,8,1 19.5   4,8,1 23.7   1,8,1 27.4
-//                 16 of 2112 x 7168           1,8,1 8.8    2,8,1 9.7
-//   tiles of 4    one of 2112 x 7168          1,8,2 6.0    2,8,2 7.0    2,4,1 10.3
-//                 one of 7168 x 16384         2,8,2 13.8   1,8,2 14.1   2,4,1 20.5
-//                 the same of int4            2,8,2 15.6   1,8,2 18.3   2,4,1 28.4
-//                 one of 65536 x 7168         2,4,2 36.6   2,4,1 39.3   2,8,2 49.4
+//   tiles of 16   64 tokens of 4096 x 7168    4,8,1 11.2   2,4,1 12.8   4,4,1 15.0
+//                 128 tokens of the same      4,4,1 16.6   4,8,1 18.6   2,4,1 22.2
+//                 16 of 65536 x 7168          4,4,1 50     4,8,1 54     2,4,1 59
+//                 16 of 7168 x 16384          2,8,1 19.3   4,8,1 23.8   1,8,1 26.8
+//                 16 of 2112 x 7168           1,8,1 8.8    2,8,1 9.6
+//   tiles of 4    one of 2112 x 7168          1,8,2 6.0    2,8,2 7.0    2,4,1 11.0
+//                 one of 7168 x 16384         2,8,2 13.7   1,8,2 14.1   2,4,1 22.0
+//                 the same of int4            2,8,2 16.0   1,8,2 16.8   2,4,1 27.9
+//                 one of 65536 x 7168         2,4,2 36.6   2,4,1 38.8   2,8,2 49.4
 // With K up to 4096 a wave of four has at most four pieces, and room for more only
-// costs occupancy: one token of 57344 x 2048 of int4 2,4,1 17.4, 2,4,2 18.6, the 8
-// experts of one token 18.8 and 20.9; so it does for tiles of 8 (8 tokens of 64
-// experts of 2048 x 4096 31.7 and 36.9).
+// costs occupancy: one token of 57344 x 2048 of int4 2,4,1 17.0, 2,4,2 18.4, the 8
+// experts of one token (7165 x 2048, int4) 19.6 and 21.7; so it does for tiles of 8 (8
+// tokens of 8 of 64 experts of 2048 x 4096 36.5 and 42.1).  By choice the tiles are as
+// many as there can be, copies of c for choices of other experts among them.
 template <int TILE>
 int launch_tile(const GemvParams& p, int group, long long tiles, int num_cus, hipStream_t st) {
   auto full = [&](int rt) { return tiles * ((p.N + 16 * rt - 1) / (16 * rt)) > num_cus; };
@@ -562,7 +565,7 @@ int launch_tile(const GemvParams& p, int group, long long tiles, int num_cus, hi
 
 // Tokens per tile: those of a small batch (an expert has no more of them, unless a
 // token's choices repeat it).  Tiles of 4 and 8 take 2 and 4 KB of LDS for x per piece
-// against 8: one token of 7168 x 16384 13.8 us, in the tile of 16's best form 19.5.
+// against 8: one token of 7168 x 16384 13.8 us, 16 in their tile's best form 19.3.
 int tile_of(int tokens) { return tokens <= 4 ? 4 : (tokens <= 8 ? 8 : 16); }
 
 int launch_tiles(const GemvParams& p, int group, int tile, long long tiles, int num_cus, hipStream_t st) {
@@ -588,9 +591,12 @@ int launch_choices(GemvParams p, int group, int tile, int n, const int32_t* ids,
     p.i0 = i;
     p.n = step;
     // experts with several tiles each, as for the dense product (256 tokens of 2 of 8
-    // experts of 14336 x 4096 190 us against 200 with streaming loads, 512 of 8 of 128, 32
-    // here, of 4096 x 7168 224 against 247); with about one tile each streaming is better
-    // (64 and 128 tokens of the same 95 us against 103, 111 against 115)
+    // experts of 14336 x 4096 182 us against 191 with streaming loads, 256 and 512 of 8 of
+    // 128, 32 here, of 4096 x 7168 146 against 152, 224 against 250); with about one tile
+    // each streaming is better (64 and 128 tokens of the same 93 us against 100, 111
+    // against 113).  The choices of all experts are counted: of 64 tokens with all of 32
+    // experts here half of the experts have two tiles, and are streamed all the same (131
+    // against 126)
     p.again = step > 2LL * tile * p.G;
     p.ids = ids + i;
     p.layout = nullptr;
@@ -665,8 +671,8 @@ int dense(GemvParams& p, int group, int M, const void* scales, size_t scale_size
   if (e != DG_OK) return e;
   const int tile = tile_of(M);
   // more tiles than one read the weights again, from the caches if the first leaves them
-  // there: 64 tokens of 4096 x 7168 11.2 us against 12.2 with streaming loads, 128 16.6
-  // against 18.5
+  // there: 64 tokens of 4096 x 7168 11.0 us against 12.1 with streaming loads, 128 16.5
+  // against 19.1
   p.again = M > tile;
   return launch_tiles(p, group, tile, ((long long)M + tile - 1) / tile, sc.num_cus, st);
 }

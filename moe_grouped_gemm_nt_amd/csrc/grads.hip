@@ -114,8 +114,8 @@ __device__ __forceinline__ double chunk_squares(const Grads& g, int i, int chunk
   return whole + (int)threadIdx.x < n ? square(sum, x[whole + threadIdx.x]) : sum;
 }
 
-// Bound by memory: 940 MB in 166 us (5.7 TB/s).  Streaming loads take 149, but leave
-// nothing in the last-level cache for the clipping: together 443 us against 433.
+// Bound by memory: 940 MB in 160 us (5.9 TB/s).  Streaming loads take 142, but leave
+// nothing in the last-level cache for the clipping: together 441 us against 424.
 //
 // Squares are summed in fp64, where those of the largest and the smallest fp32
 // values still differ from infinity and zero; one partial sum per workgroup, added
@@ -191,8 +191,9 @@ __device__ __forceinline__ void chunk_scale(const Grads& g, int i, int chunk, fl
   if (whole + (int)threadIdx.x < n) y[whole + threadIdx.x] = scaled(x[whole + threadIdx.x], factor);
 }
 
-// Bound by memory: 940 MB read and written in 310 us (6.1 TB/s; a device copy reaches
-// 5.1), with streaming loads and stores.
+// Bound by memory: 940 MB read and written in 300 us (6.3 TB/s; a device copy reaches
+// 5.1), with streaming loads and stores; 264 behind the norm, whose reads it finds in the
+// last-level cache for a part.
 __global__ __launch_bounds__(THREADS) void grad_clip_kernel(Grads g) {
   const float norm = *g.norm;
   const float q = g.max_norm / (norm + 1e-6f);
@@ -207,8 +208,8 @@ __global__ __launch_bounds__(THREADS) void grad_clip_kernel(Grads g) {
 }
 
 // Workgroups per CU: few for the norm, each of which leaves a partial sum (940 MB in
-// 166 us, with 256 per CU in 231), as good as one per chunk for the clipping (310 us,
-// with 64 315, with 8 and chunks of twice the size 342).
+// 160 us, with 256 per CU in 226), as good as one per chunk for the clipping (norm and
+// clipping together 424 us, with 64 437, with 8 and chunks of twice the size 460).
 constexpr int kNormGroups = 8, kClipGroups = 256;
 constexpr long long kMaxBytes = 1LL << 45;
 constexpr int kMaxTensors = 1 << 20;
