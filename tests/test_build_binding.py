@@ -44,6 +44,7 @@ def without_headers(monkeypatch):
     monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": "/nowhere"})
 
 
+@pytest.mark.skipif(build.binding_lacks() is not None, reason="the native side cannot be built here")
 def test_all_there(tree):
     folder, commands = tree
     assert build.build() == str(folder / "libdg.so")
@@ -62,6 +63,7 @@ def test_the_library_is_built_without(tree, monkeypatch, capsys, missing):
     assert "_binding.so" in capsys.readouterr().err
 
 
+@pytest.mark.skipif(build.binding_lacks() is not None, reason="the native side cannot be built here")
 def test_an_error_in_the_binding_is_raised_after_the_library(tree, monkeypatch):
     folder, _ = tree
     compiler = build._run
