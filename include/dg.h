@@ -222,8 +222,7 @@ int dg_choose_config(int form, int rows, int N, int K, int num_groups, int num_c
  * verdicts; and what the operators around the products put there: the layouts'
  * counts, the scatters' block maxima, the adapters' lists and partial sums, the
  * lists of the 4-bit products by choice, the balance loss's and the norm's partial
- * sums), so
- * that calls running at the same time on different streams no longer share
+ * sums), so that calls running at the same time on different streams no longer share
  * scratch memory. workspace: device memory on the current device, 256-byte
  * aligned, at least 256 bytes (the verdicts). A workspace of at least 256 +
  * 4096 bytes also holds, after the verdicts, the 4096 bytes of counters of the
@@ -439,11 +438,11 @@ int dg_lora_bf16_nt(const void* x, int ldx, const void* a, const void* b, const 
  * token's logits lie; shares below 2^-126 are 0.  Shares are fp32 and summed in
  * fp32 over stretches of tokens, two per CU (a small bound workspace makes them
  * longer), and those sums and the loss in fp64: with 256 CUs and the device's
- * workspace a loss is off by less than (E + 160 + T / 4096) * 2^-24 of itself.  E
- * at most 1024, top_k at most
- * 64, T * top_k at most 2^30 (DG_ERR_UNSUPPORTED otherwise).  Scratch: workspace
- * (DG_ERR_UNSUPPORTED if a bound one has no room for 16 bytes per expert, their
- * number rounded up to a multiple of 4).  Returns a dg_status. */
+ * workspace a loss is off by less than (E + 160 + T / 4096) * 2^-24 of itself.
+ * E at most 1024, top_k at most 64, T * top_k at most 2^30 (DG_ERR_UNSUPPORTED
+ * otherwise).  Scratch: workspace (DG_ERR_UNSUPPORTED if a bound one has no room
+ * for 16 bytes per expert, their number rounded up to a multiple of 4).  Returns a
+ * dg_status. */
 int dg_route_balance(const void* logits, int logits_type, const int32_t* topk_ids, const int32_t* seq_starts,
                      float* loss, int32_t* counts, int T, int E, int top_k, int num_seqs, int score, float scale,
                      void* stream);
@@ -531,9 +530,8 @@ int dg_grad_norm(const void* const* grads, const int* types, const long long* si
 /* The gradients scaled so that their norm is at most max_norm:
  *   out[i][j] = grads[i][j] * f,   f = min(1, max_norm / (norm[0] + 1e-6))
  * f and the products in fp32, those of bf16 tensors rounded once more to bf16.  norm
- * is read by the kernels only,
- * so that a job may sum the squares of several GPUs in between.  A NaN norm makes f
- * NaN, an infinite one 0.
+ * is read by the kernels only, so that a job may sum the squares of several GPUs in
+ * between.  A NaN norm makes f NaN, an infinite one 0.
  *   grads, types, sizes as above; out num_tensors addresses on the HOST: each may
  *   equal grads[i], and otherwise shares no memory with any tensor or with norm
  *   (DG_ERR_INVALID_ARG otherwise).  max_norm must not be negative.
